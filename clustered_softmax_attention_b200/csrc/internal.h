@@ -177,4 +177,30 @@ cudaError_t run_diag_merge(const void *Q, const void *K, const void *V, int dtyp
                            int N, int P, int block, int levels, float scale,
                            const float *part_o, const float *part_lse, void *O, cudaStream_t st);
 
+// ---------------------------------------------------------------------------
+// Serving: rotary positions (rope.cu), the 4-bit cache (cache.cu), attention over it
+// (cache_attend.cu).  Arguments are validated in serving_api.cu.
+// ---------------------------------------------------------------------------
+// Phase table of a muse_rope: pair i turns by pos * turn[i] / 2^64 of a turn.
+struct RopeTable {
+  int P;           // pairs
+  int axes;
+  bool adjacent;   // pairs (2i, 2i + 1) instead of (i, i + P)
+  uint64_t turn[64];
+  uint8_t axis[64];
+};
+cudaError_t run_rope(const muse_rows &Q, const muse_rows &K, int Hk, const muse_dims &d,
+                     const int32_t *pos, int pos_batches, const RopeTable &t, const muse_rows &Qo,
+                     const muse_rows &Ko, cudaStream_t st);
+cudaError_t run_cache_write(const muse_rows &K, const muse_rows &V, const muse_dims &d,
+                            const muse_cache &c, const int32_t *start, const int32_t *counts,
+                            int *status, cudaStream_t st);
+cudaError_t run_cache_read(const muse_dims &d, const muse_cache &c, const int32_t *start,
+                           const int32_t *counts, const muse_rows &K, const muse_rows &V,
+                           int *status, cudaStream_t st);
+size_t cache_attend_ws(const muse_dims &d, int Hkv);
+cudaError_t run_cache_attend(const muse_rows &Q, const muse_dims &d, const muse_cache &c,
+                             const int32_t *lens, const int32_t *counts, const muse_rows &O,
+                             float *lse, void *ws, int *status, cudaStream_t st);
+
 }  // namespace muse

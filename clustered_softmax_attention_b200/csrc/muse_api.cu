@@ -425,6 +425,8 @@ extern "C" size_t muse_workspace_size(const char *entry, muse_dims d, int Cq, in
   const bool dv_needed = strcmp(entry, "muse_kmeans") != 0;
   if (check_dims(d, dv_needed) != MUSE_OK) return 0;
   if (!strcmp(entry, "muse_kmeans")) return valid_C(Cq, d.N) ? ws_kmeans(d, Cq) : 0;
+  if (!strcmp(entry, "muse_cache_attend"))
+    return d.N <= MUSE_CACHE_MAX_ROWS && Cq >= 1 && d.H % Cq == 0 ? cache_attend_ws(d, Cq) : 0;
   if (!valid_C(Cq, d.N) && strcmp(entry, "muse_causal_blocks") != 0) return 0;
   if (!strcmp(entry, "muse_tilted_summaries"))
     return valid_C(Ck, d.N) ? ws_summaries(d, Cq, Ck, true, true) : 0;

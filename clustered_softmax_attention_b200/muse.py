@@ -37,6 +37,23 @@ class MuseDims(ctypes.Structure):
                 ("scale", ctypes.c_float)]
 
 
+class MuseRows(ctypes.Structure):
+    """muse_rows: a pointer and the strides of batch, head and row, in elements."""
+    _fields_ = [("p", ctypes.c_void_p), ("sb", ctypes.c_int64), ("sh", ctypes.c_int64),
+                ("sn", ctypes.c_int64)]
+
+
+class MuseRope(ctypes.Structure):
+    _fields_ = [("axes", ctypes.c_int), ("sections", ctypes.c_int * 4), ("base", ctypes.c_double),
+                ("flags", ctypes.c_uint)]
+
+
+class MuseCache(ctypes.Structure):
+    _fields_ = [("tiles", ctypes.c_void_p), ("page_table", ctypes.c_void_p),
+                ("pages", ctypes.c_int), ("Hkv", ctypes.c_int), ("page", ctypes.c_int),
+                ("max_pages", ctypes.c_int)]
+
+
 _vp, _i, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
 _SIGS = {
     "muse_kmeans": [_vp, MuseDims, _i, _i, _vp, _vp, _vp, _vp, _vp, _sz, _vp],
@@ -60,8 +77,14 @@ _SIGS = {
     "muse_refine_form": [MuseDims, _i, _i, ctypes.c_uint],
     "muse_backward": [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, MuseDims, _i, _i, _vp, _vp, _vp,
                       _vp, _sz, _vp],
+    "muse_rope_axes": [MuseRows, MuseRows, _i, MuseDims, _vp, _i, MuseRope, MuseRows, MuseRows,
+                       _vp],
+    "muse_cache_tile_bytes": [_i, _i],
+    "muse_cache_write": [MuseRows, MuseRows, MuseDims, MuseCache, _vp, _vp, _vp],
+    "muse_cache_read": [MuseDims, MuseCache, _vp, _vp, MuseRows, MuseRows, _vp],
+    "muse_cache_attend": [MuseRows, MuseDims, MuseCache, _vp, _vp, MuseRows, _vp, _vp, _sz, _vp],
 }
-_RES = {"muse_workspace_size": _sz, "muse_status_string": ctypes.c_char_p,
+_RES = {"muse_workspace_size": _sz, "muse_cache_tile_bytes": _sz, "muse_status_string": ctypes.c_char_p,
         "muse_causal_levels": _i, "muse_last_error_detail": ctypes.c_char_p}
 
 
@@ -369,3 +392,199 @@ def muse_backward(Q, K, V, dO, q_perm, q_offsets, k_perm, k_offsets, scale: floa
                                _p(k_offsets), d, Cq, Ck, _p(dQ), _p(dK), _p(dV), _p(ws), ws.numel(),
                                _stream()), "muse_backward")
     return dQ, dK, dV
+
+
+# ---------------------------------------------------------------------------------------
+# Serving: rotary positions, the 4-bit cache, attention over it.
+#
+# These take rows as they lie (any batch, head and row strides that are multiples of 16 bytes,
+# the last dimension dense) and run on the current stream of the tensors' device.
+# ---------------------------------------------------------------------------------------
+MUSE_ROPE_INVERSE = 1
+MUSE_ROPE_ADJACENT = 2
+MUSE_ROPE_AXIS_LADDER = 4
+MUSE_CACHE_MAX_ROWS = 128
+_ITEM = {torch.float32: 4, torch.bfloat16: 2}
+
+
+def _rows(t: torch.Tensor, name: str, written: bool = False) -> MuseRows:
+    """The view of a [B,H,N,D] tensor; a dimension of size 1 has no stride of its own."""
+    B, H, N, D = t.shape
+    s = t.stride()
+    if not t.is_cuda:
+        raise ValueError(f"{name}: expected a CUDA tensor")
+    sb, sh, sn = s[0] if B > 1 else 0, s[1] if H > 1 else 0, s[2] if N > 1 else 0
+    unit = 16 // _ITEM[t.dtype]
+    if s[3] != 1 or (sb | sh | sn) % unit or t.data_ptr() % 16:
+        raise ValueError(f"{name}: rows must be dense and 16-byte aligned, strides {tuple(s)}")
+    if written:
+        end = D  # rows that are written must not overlap: each stride clears what is below it
+        for st, n in sorted(x for x in ((sb, B), (sh, H), (sn, N)) if x[1] > 1):
+            if st < end:
+                raise ValueError(f"{name}: overlapping rows, strides {tuple(s)}")
+            end = st * (n - 1) + end
+    return MuseRows(t.data_ptr(), sb, sh, sn)
+
+
+def _ints(t: Optional[torch.Tensor], shape, name: str, device) -> Optional[int]:
+    if t is None:
+        return None
+    if tuple(t.shape) != tuple(shape) or t.dtype != torch.int32 or not t.is_contiguous() \
+            or t.device != device:
+        raise ValueError(f"{name}: expected a contiguous int32 tensor {list(shape)} on {device}, "
+                         f"got {t.dtype} {list(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def _four(t: torch.Tensor, name: str, shape, like: torch.Tensor):
+    if t.dim() != 4 or any(a is not None and a != b for a, b in zip(shape, t.shape)):
+        want = "[" + ",".join("." if a is None else str(a) for a in shape) + "]"
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {want}")
+    if t.dtype != like.dtype or t.device != like.device:
+        raise ValueError(f"{name}: {t.dtype} on {t.device}, expected {like.dtype} on {like.device}")
+
+
+def _call(fn: str, device, *args):
+    """The call on the current stream of `device`, with that device current."""
+    f = getattr(lib(), fn)
+    st = torch.cuda.current_stream(device).cuda_stream
+    if torch.cuda.current_device() == device.index:
+        code = f(*args, st)
+    else:
+        with torch.cuda.device(device):
+            code = f(*args, st)
+    if code:
+        _check(code, fn)
+
+
+def muse_rope_axes(Q, positions, sections, base: float = 10000.0, K=None, flags: int = 0,
+                   out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None):
+    """Rotary positions with several axes: Q [B,H,N,D] (and K [B,Hk,N,D]) turned by positions
+    int32 [B,axes,N] (or [axes,N], shared by the batch); sections: the pairs of each axis.
+    Returns out, or (out, k_out) with K.  out may be Q itself, k_out K itself.  With
+    MUSE_ROPE_INVERSE it turns back, which is the gradient."""
+    if Q.dim() != 4 or Q.dtype not in _ITEM:
+        raise ValueError(f"Q: expected float32 or bfloat16 [B,H,N,D], got {Q.dtype} {tuple(Q.shape)}")
+    B, H, N, D = Q.shape
+    axes = len(sections)
+    if not 1 <= axes <= 4:
+        raise ValueError(f"sections: 1 to 4 axes, got {axes}")
+    nb = 1 if positions.dim() == 2 else B
+    pos = _ints(positions, (axes, N) if positions.dim() == 2 else (B, axes, N), "positions", Q.device)
+    if out is None:
+        out = torch.empty((B, H, N, D), dtype=Q.dtype, device=Q.device)
+    _four(out, "out", (B, H, N, D), Q)
+    pairs = [(Q, out, "out")]
+    if K is not None:
+        _four(K, "K", (B, None, N, D), Q)
+        if k_out is None:
+            k_out = torch.empty(K.shape, dtype=Q.dtype, device=Q.device)
+        _four(k_out, "k_out", K.shape, Q)
+        pairs.append((K, k_out, "k_out"))
+    for x, y, name in pairs:
+        if x.data_ptr() == y.data_ptr() and x.stride() != y.stride():
+            raise ValueError(f"{name}: in place needs the strides of its input")
+    q, qo = _rows(Q, "Q"), _rows(out, "out", True)
+    k, ko, Hk = MuseRows(), MuseRows(), 0
+    if K is not None:
+        k, ko, Hk = _rows(K, "K"), _rows(k_out, "k_out", True), K.shape[1]
+    r = MuseRope(axes, (ctypes.c_int * 4)(*sections), float(base), flags)
+    _call("muse_rope_axes", Q.device, q, k, Hk, MuseDims(B, H, N, D, D, _dtype_code(Q), 1.0), pos, nb,
+          r, qo, ko)
+    return out if K is None else (out, k_out)
+
+
+def muse_cache_tile_bytes(D: int, Dv: int) -> int:
+    return int(lib().muse_cache_tile_bytes(D, Dv))
+
+
+def muse_cache_shape(pages: int, Hkv: int, page: int, D: int, Dv: int):
+    """Shape of the uint8 tensor that holds a cache: [pages, Hkv, page/32, tile bytes]."""
+    n = muse_cache_tile_bytes(D, Dv)
+    if n == 0 or page % 32:
+        raise MuseError(2, "muse_cache_shape")
+    return pages, Hkv, page // 32, n
+
+
+def _cache(cache: torch.Tensor, page_table: torch.Tensor, B: int, D: int, like: torch.Tensor):
+    """(muse_cache, Dv) of a cache tensor and its page table."""
+    if cache.dim() != 4 or cache.dtype != torch.uint8 or not cache.is_contiguous() \
+            or cache.device != like.device:
+        raise ValueError(f"cache: expected a contiguous uint8 tensor [pages,Hkv,page/32,bytes] on "
+                         f"{like.device}, got {cache.dtype} {list(cache.shape)} on {cache.device}")
+    if page_table.dim() != 2:
+        raise ValueError(f"page_table: expected [B,max_pages], got {list(page_table.shape)}")
+    pages, Hkv, tiles, size = cache.shape
+    Dv = size // 18 - D
+    if size % 18 or D not in (64, 128) or Dv not in (64, 128):
+        raise ValueError(f"cache: tiles of {size} bytes do not hold keys of width {D}")
+    table = _ints(page_table, (B, page_table.shape[1]), "page_table", like.device)
+    return MuseCache(cache.data_ptr(), table, pages, Hkv, tiles * 32, page_table.shape[1]), Dv
+
+
+def muse_cache_write(cache, K, V, page_table, start, counts=None):
+    """K [B,Hkv,N,D], V [B,Hkv,N,Dv] into the 4-bit cache as tokens start[b] + n, n < counts[b]
+    (all N without counts).  Returns the cache."""
+    if K.dim() != 4 or K.dtype not in _ITEM:
+        raise ValueError(f"K: expected float32 or bfloat16 [B,Hkv,N,D], got {K.dtype} {tuple(K.shape)}")
+    B, H, N, D = K.shape
+    c, Dv = _cache(cache, page_table, B, D, K)
+    _four(K, "K", (B, c.Hkv, N, D), K)
+    _four(V, "V", (B, H, N, Dv), K)
+    _call("muse_cache_write", K.device, _rows(K, "K"), _rows(V, "V"),
+          MuseDims(B, H, N, D, Dv, _dtype_code(K), 1.0), c, _ints(start, (B,), "start", K.device),
+          _ints(counts, (B,), "counts", K.device))
+    return cache
+
+
+def muse_cache_read(cache, page_table, start, N: int, D: int, dtype=torch.bfloat16, counts=None,
+                    out=None):
+    """(K [B,Hkv,N,D], V [B,Hkv,N,Dv]) of tokens start[b] + n, n < counts[b]; rows from counts[b]
+    on are left as they are (zero in tensors made here).  out: a (K, V) to read into."""
+    B = page_table.shape[0]
+    c, Dv = _cache(cache, page_table, B, D, cache)
+    if out is None:
+        new = torch.empty if counts is None else torch.zeros
+        out = tuple(new((B, c.Hkv, N, w), dtype=dtype, device=cache.device) for w in (D, Dv))
+    K, V = out
+    if K.dtype not in _ITEM:
+        raise ValueError(f"K: expected float32 or bfloat16, got {K.dtype}")
+    _four(K, "K", (B, c.Hkv, N, D), K)
+    _four(V, "V", (B, c.Hkv, N, Dv), K)
+    if K.device != cache.device:
+        raise ValueError(f"K: on {K.device}, the cache on {cache.device}")
+    _call("muse_cache_read", cache.device, MuseDims(B, c.Hkv, N, D, Dv, _dtype_code(K), 1.0), c,
+          _ints(start, (B,), "start", cache.device), _ints(counts, (B,), "counts", cache.device),
+          _rows(K, "K", True), _rows(V, "V", True))
+    return K, V
+
+
+def muse_cache_attend(Q, cache, page_table, lens, counts=None, scale: float = 1.0,
+                      out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                      ws: Optional[torch.Tensor] = None):
+    """Causal attention of the newest rows Q [B,H,N,D] of every sequence over its cache: row m is
+    token lens[b] - counts[b] + m (counts[b] = N without counts).  Returns (out [B,H,N,Dv],
+    lse float32 [B,H,N]); rows from counts[b] on are left as they are (zero in tensors made
+    here)."""
+    if Q.dim() != 4 or Q.dtype not in _ITEM:
+        raise ValueError(f"Q: expected float32 or bfloat16 [B,H,N,D], got {Q.dtype} {tuple(Q.shape)}")
+    B, H, N, D = Q.shape
+    c, Dv = _cache(cache, page_table, B, D, Q)
+    new = torch.empty if counts is None else torch.zeros
+    if out is None:
+        out = new((B, H, N, Dv), dtype=Q.dtype, device=Q.device)
+    if lse is None:
+        lse = new((B, H, N), dtype=torch.float32, device=Q.device)
+    _four(out, "out", (B, H, N, Dv), Q)
+    if tuple(lse.shape) != (B, H, N) or lse.dtype != torch.float32 or not lse.is_contiguous() \
+            or lse.device != Q.device:
+        raise ValueError(f"lse: expected a contiguous float32 tensor {[B, H, N]} on {Q.device}")
+    d = MuseDims(B, H, N, D, Dv, _dtype_code(Q), float(scale))
+    if ws is None:
+        ws = workspace("muse_cache_attend", d, c.Hkv, device=Q.device)
+    elif ws.dtype != torch.uint8 or not ws.is_contiguous() or ws.device != Q.device:
+        raise ValueError(f"ws: expected a contiguous uint8 tensor on {Q.device}")
+    _call("muse_cache_attend", Q.device, _rows(Q, "Q"), d, c, _ints(lens, (B,), "lens", Q.device),
+          _ints(counts, (B,), "counts", Q.device), _rows(out, "out", True), lse.data_ptr(),
+          ws.data_ptr(), ws.numel())
+    return out, lse

@@ -310,10 +310,121 @@ muse_status muse_backward(const void *Q, const void *K, const void *V, const voi
                           void *dK, void *dV, void *ws, size_t ws_bytes, muse_stream_t st);
 
 /*
+ * Serving: rotary positions, a key/value cache held in 4 bits, and attention over it
+ * ----------------------------------------------------------------------------------
+ * What a program that generates needs around the entry points above: positions turned into
+ * Q and K before they are clustered or cached, and, once muse_causal_blocks or
+ * muse_retrieve_exact has been over a prompt, a cache from which the next tokens are
+ * answered.  The pages describe the forward pass only and have no counterpart of these.
+ *
+ * Rows are given by a view: the element (b, h, n, c) of a tensor is at
+ * p + (b*sb + h*sh + n*sn + c) * element size.  p is 16-byte aligned and every stride a
+ * multiple of 16 bytes (so a projection's [B,N,H,D] output is read where it is); for what is
+ * read a stride may be 0 (a broadcast tensor), rows that are written must not overlap.
+ */
+typedef struct {
+  void *p;            /* not written through where the argument is an input */
+  int64_t sb, sh, sn; /* strides in elements */
+} muse_rows;
+
+/*
+ * muse_rope_axes - rotary positions with several axes: Qo = R Q and, when K.p is not NULL,
+ * Ko = R K for Q [B,H,N,D] and K [B,Hk,N,D].
+ *   P = sum(sections) channel pairs turn, the other D - 2P channels are copied.  Pair i
+ *   belongs to axis a(i) (sections[0] pairs to axis 0, the next sections[1] to axis 1, ...)
+ *   and is turned by the angle t = pos[b, a(i), n] * base^(-e(i)):
+ *     (x, y) -> (x cos t - y sin t, x sin t + y cos t),
+ *   e(i) = i / P, or with MUSE_ROPE_AXIS_LADDER (i - first pair of a(i)) / sections[a(i)].
+ *   Pair i is the channels (i, i + P), or (2i, 2i + 1) with MUSE_ROPE_ADJACENT.
+ *   MUSE_ROPE_INVERSE turns by -t: R is orthogonal, so that is also the gradient (dQ = R^T
+ *   dQo).  The angle is reduced exactly for every int32 position: a turn is 2^64 and
+ *   pos * (frequency as a 64-bit fraction of a turn) is taken modulo 2^64.
+ * d.H counts Q's heads, Hk K's (ignored without K); d.Dv and d.scale are ignored.  pos is
+ * int32 [pos_batches, axes, N] with pos_batches = B, or 1 (shared by the batch); text tokens
+ * have one axis, or the same position on all.  Qo may be Q itself (p and strides equal), Ko
+ * K itself; any other overlap is undefined.  1 <= axes <= 4, every section >= 1, P <= D/2,
+ * 1 <= base <= 1e12.
+ */
+#define MUSE_ROPE_MAX_AXES 4
+#define MUSE_ROPE_INVERSE 1u
+#define MUSE_ROPE_ADJACENT 2u
+#define MUSE_ROPE_AXIS_LADDER 4u
+typedef struct {
+  int axes;
+  int sections[MUSE_ROPE_MAX_AXES]; /* pairs of each axis */
+  double base;
+  unsigned flags;
+} muse_rope;
+muse_status muse_rope_axes(muse_rows Q, muse_rows K, int Hk, muse_dims d, const int32_t *pos,
+                           int pos_batches, muse_rope r, muse_rows Qo, muse_rows Ko,
+                           muse_stream_t st);
+
+/*
+ * The cache: `tiles` is uint8 [pages, Hkv, page/32, muse_cache_tile_bytes(D, Dv)]; token t of
+ * sequence b lives in page page_table[b, t / page] (int32 [B, max_pages]).  page is a power of
+ * two, 32..1024.  pages * Hkv * page / 32 < 2^31, max_pages * page < 2^31.
+ *   Values.  32 neighbouring channels of one token and head are a group: step = the bfloat16
+ *   nearest to max|x| / 7, code = x / step rounded to the nearest integer, ties to even, in
+ *   -7..7; the value held is code * step.  A group with an infinity or a NaN is held as NaN;
+ *   a step of 0 holds zeros.  9/16 byte a value with the steps.
+ *   A tile holds 32 tokens of one head: key codes (16 D bytes), value codes (16 Dv bytes), key
+ *   steps bfloat16 [32, D/32], value steps bfloat16 [32, Dv/32].  Codes are four bits (code +
+ *   8), eight to a 32-bit word, the first in the lowest bits.  Index of the word and the
+ *   channels of token t in it:
+ *     keys, D = 128:   16 t + 4 q + w,                     channels 32 w + 8 q + (0..7)
+ *     keys, D = 64:    128 (t/16) + 16 (t%8) + 4 q + 2 (t/8%2) + w,        the same channels
+ *     values, Dv = 128: 128 (t/8) + 16 g + 4 (t%8/2) + 2 (t%2) + w, channels 64 w + g + 8 (0..7)
+ *     values, Dv = 64: 128 (t/16) + 16 g + 4 (t%8/2) + 2 (t/8%2) + t%2,  channels g + 8 (0..7)
+ *   so that 16 bytes a lane are operands of a matrix instruction without further exchange.
+ * Sequences must not share a page that is being written.  Values past a sequence's end are
+ * never used, whatever they are.
+ */
+typedef struct {
+  void *tiles;
+  const int32_t *page_table;
+  int pages, Hkv, page, max_pages;
+} muse_cache;
+size_t muse_cache_tile_bytes(int D, int Dv); /* 18 (D + Dv); 0 for other widths */
+
+/*
+ * muse_cache_write - K [B,Hkv,N,D], V [B,Hkv,N,Dv] (d.H = c.Hkv) into the cache: row n < counts[b]
+ * of sequence b becomes token start[b] + n.  counts int32 [B], or NULL (N for every sequence):
+ * rows from counts[b] on are not read, and tokens before start[b] stay as they are.
+ * muse_cache_read - the other way: row n < counts[b] of K and V becomes token start[b] + n, its value
+ * rounded to d.dtype; rows from counts[b] on stay as they are.
+ * A token whose position or page lies outside the table or the cache, or a count outside 0..N,
+ * sets MUSE_ERR_DEVICE in the device status word; the token is left out (the count clamped).
+ * d.scale is ignored.
+ */
+muse_status muse_cache_write(muse_rows K, muse_rows V, muse_dims d, muse_cache c,
+                             const int32_t *start, const int32_t *counts, muse_stream_t st);
+muse_status muse_cache_read(muse_dims d, muse_cache c, const int32_t *start, const int32_t *counts,
+                            muse_rows K, muse_rows V, muse_stream_t st);
+
+/*
+ * muse_cache_attend - causal attention of the newest N rows of every sequence over its cache:
+ *   row m < counts[b] of sequence b (counts NULL: N) is token lens[b] - counts[b] + m, and with
+ *   k_t, v_t the values held
+ *     O = sum_t p_t v_t, p = softmax_t(s q.k_t) over t <= lens[b] - counts[b] + m, t < lens[b];
+ *     lse = log sum_t exp(s q.k_t).
+ *   Query head h of d.H reads cache head h / (d.H / c.Hkv).  A row that sees nothing (a sequence
+ *   shorter than its new rows) gives O = 0 and lse = -inf; rows from counts[b] on stay as they are.
+ * Q [B,H,N,D], O [B,H,N,Dv], 1 <= N <= 128, d.H a multiple of c.Hkv; lse float32 [B,H,N] dense,
+ * or NULL.  The codes enter the products as they are (integers), the steps in float32.
+ * A length below 0 or past the table, or a page outside the cache, sets MUSE_ERR_DEVICE; those
+ * tokens are left out.  Workspace: muse_workspace_size("muse_cache_attend", d, c.Hkv, ...); the
+ * library leaves nothing in it that the next call needs.
+ */
+#define MUSE_CACHE_MAX_ROWS 128
+muse_status muse_cache_attend(muse_rows Q, muse_dims d, muse_cache c, const int32_t *lens,
+                              const int32_t *counts, muse_rows O, float *lse, void *ws,
+                              size_t ws_bytes, muse_stream_t st);
+
+/*
  * muse_workspace_size - bytes of workspace `entry` needs ("muse_kmeans" with C = Cq,
  * "muse_tilted_summaries", "muse_dipole_refine", "muse_forward", "muse_forward_ex",
- * "muse_causal_blocks", "muse_retrieve_exact", "muse_backward").  Arguments an entry does not
- * use are ignored.  Returns 0 for an unknown entry or invalid sizes.
+ * "muse_causal_blocks", "muse_retrieve_exact", "muse_backward", "muse_cache_attend" with the
+ * cache's heads as Cq).  Arguments an entry does not use are ignored.  Returns 0 for an unknown entry or invalid sizes.
  */
 size_t muse_workspace_size(const char *entry, muse_dims d, int Cq, int Ck, int block, int k1,
                            int k2);

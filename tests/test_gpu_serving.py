@@ -1,0 +1,585 @@
+"""Rotary positions, the 4-bit cache and attention over it, against the float64 oracle.
+
+Tolerances are worst-case bounds written beside each comparison: u = 2^-24 is half a float32
+step, h = 2^-8 half a bfloat16 step (relative)."""
+import numpy as np
+import pytest
+import torch
+
+from clustered_softmax_attention_b200 import muse as m
+from oracle import serving_oracle as so
+
+pytestmark = pytest.mark.gpu
+
+U, HALF = 2.0 ** -24, {torch.float32: 2.0 ** -24, torch.bfloat16: 2.0 ** -8}
+F32, BF16 = torch.float32, torch.bfloat16
+
+
+def host(t):
+    return t.detach().to(torch.float64).cpu().numpy()
+
+
+def randn(seed, *shape, dtype=F32):
+    g = torch.Generator().manual_seed(seed)
+    return torch.randn(*shape, generator=g).to(dtype).cuda()
+
+
+def ints(x):
+    return torch.tensor(np.asarray(x), dtype=torch.int32).cuda()
+
+
+def ok():
+    assert m.muse_last_device_status() == 0
+
+
+# ------------------------------------------------------------------- rotary positions
+
+def rope_close(got, X, pos, sections, base, dtype, **kw):
+    """The angle is off by at most u half turns (its rounding to float32) and sincospif by two
+    steps (2^-22), the position's product with a float64 frequency by |pos| 2^-53; two products
+    and a sum round three more times; the result once to its type."""
+    ref = so.rope(X, pos, sections, base, **kw)
+    size = np.abs(X).max(-1, keepdims=True) * 2
+    far = np.abs(np.asarray(pos, dtype=np.float64)).max() * 2.0 ** -53
+    tol = HALF[dtype] * np.abs(ref) + size * (np.pi * U + 2.0 ** -22 + 3 * U + far)
+    assert (np.abs(got - ref) <= tol).all(), np.max(np.abs(got - ref) - tol)
+
+
+ROPE = [  # B, H, Hk, N, D, sections, base, span of positions
+    (1, 1, 0, 1, 64, (32,), 1e4, 1 << 31),
+    (2, 3, 1, 37, 64, (8, 12, 12), 1e4, 2000),
+    (3, 8, 2, 5, 128, (16, 24, 24), 5e5, 1 << 31),
+    (1, 4, 4, 130, 128, (24, 24), 100.0, 1 << 20),
+    (2, 2, 2, 33, 128, (1, 2, 3, 5), 1.0, 50),
+    (1, 5, 0, 7, 64, (1,), 1e12, 1 << 31),
+    (2, 9, 3, 64, 128, (13, 17), 1e4, 300),
+]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("flags", range(8))
+@pytest.mark.parametrize("B,H,Hk,N,D,sections,base,span", ROPE)
+def test_rope_matches_oracle(B, H, Hk, N, D, sections, base, span, flags, dtype):
+    rng = np.random.default_rng(flags)
+    Q = randn(1, B, H, N, D, dtype=dtype)
+    K = randn(2, B, Hk, N, D, dtype=dtype) if Hk else None
+    pos = rng.integers(-span, span, (B, len(sections), N))
+    kw = dict(inverse=bool(flags & 1), adjacent=bool(flags & 2), axis_ladder=bool(flags & 4))
+    out = m.muse_rope_axes(Q, ints(pos), sections, base, K=K, flags=flags)
+    for x, y in zip((Q, K), out if Hk else (out,)):
+        rope_close(host(y), host(x), pos, sections, base, dtype, **kw)
+        P = sum(sections)
+        assert torch.equal(y[..., 2 * P:], x[..., 2 * P:])
+    ok()
+
+
+@pytest.mark.parametrize("adjacent", [0, m.MUSE_ROPE_ADJACENT])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_rope_layouts_in_place_and_shared_positions(dtype, adjacent):
+    """[B,N,H,D] memory in, shared positions, in place, a broadcast batch: the same values."""
+    B, H, N, D, sec = 3, 4, 19, 64, (10, 6, 8)
+    pos = ints(np.random.default_rng(0).integers(0, 99, (3, N)))
+    X = randn(3, B, N, 3 * H, D, dtype=dtype)
+    Q, K = X[:, :, :H].transpose(1, 2), X[:, :, H:2 * H].transpose(1, 2)
+    ref_q, ref_k = m.muse_rope_axes(Q.contiguous(), pos.expand(B, 3, N).contiguous(), sec,
+                                    K=K.contiguous(), flags=adjacent)
+    kept = X.clone()
+    a, b = m.muse_rope_axes(Q, pos, sec, K=K, flags=adjacent)
+    assert torch.equal(a, ref_q) and torch.equal(b, ref_k) and torch.equal(X, kept)
+    m.muse_rope_axes(Q, pos, sec, K=K, flags=adjacent, out=Q, k_out=K)
+    assert torch.equal(Q, ref_q) and torch.equal(K, ref_k)
+    assert torch.equal(X[:, :, 2 * H:], kept[:, :, 2 * H:])
+    one = randn(4, 1, H, N, D, dtype=dtype)
+    y = m.muse_rope_axes(one.expand(B, H, N, D), pos, sec, flags=adjacent)
+    assert torch.equal(y, m.muse_rope_axes(one, pos, sec, flags=adjacent).expand(B, H, N, D))
+    ok()
+
+
+@pytest.mark.parametrize("sections,flags", [((32,), 0), ((9, 11), 2), ((8, 12, 12), 4)])
+def test_rope_gradient_is_the_inverse(sections, flags):
+    """sum(dO * R(X)) differentiated: against central differences of the oracle, and
+    <R x, y> = <x, R^T y> on the GPU."""
+    B, H, N, D = 1, 2, 5, 64
+    rng = np.random.default_rng(7)
+    pos = rng.integers(0, 50, (B, len(sections), N))
+    X, dO = randn(5, B, H, N, D), randn(6, B, H, N, D)
+    G = host(m.muse_rope_axes(dO, ints(pos), sections, 100.0, flags=flags | m.MUSE_ROPE_INVERSE))
+    kw = dict(adjacent=bool(flags & 2), axis_ladder=bool(flags & 4))
+    f = lambda x: (so.rope(x, pos, sections, 100.0, **kw) * host(dO)).sum()
+    for idx in [(0, 0, 0, 0), (0, 1, 4, 17), (0, 0, 3, 33), (0, 1, 2, 63)]:
+        d = np.zeros((B, H, N, D))
+        d[idx] = 1e-4
+        # R is linear: the difference is exact but for float64 rounding of sums of a few hundred
+        # terms (1e-13 / 2e-4); the kernel as in rope_close
+        np.testing.assert_allclose((f(host(X) + d) - f(host(X) - d)) / 2e-4, G[idx], atol=1e-5)
+    rope_close(G, host(dO), pos, sections, 100.0, F32, inverse=True, **kw)
+
+
+def test_rope_copies_infinities_and_nan_of_untouched_channels():
+    X = randn(8, 1, 2, 9, 64, dtype=BF16)
+    X[..., 40] = float("nan")
+    X[..., 41] = float("inf")
+    for flags in (0, m.MUSE_ROPE_ADJACENT):
+        Y = m.muse_rope_axes(X, ints(np.arange(9)[None]), (20,), flags=flags)
+        assert torch.equal(Y[..., 40:].view(torch.int16), X[..., 40:].view(torch.int16))
+        assert torch.isfinite(Y[..., :40]).all()
+    ok()
+
+
+# ------------------------------------------------------------------------- the cache
+
+class Store:
+    """A cache with a shuffled page table, and what the oracle says it holds."""
+
+    def __init__(self, B, Hkv, page, max_pages, D, Dv, seed=0, spare=2, fill=0):
+        rng = np.random.default_rng(seed)
+        n = B * max_pages + spare
+        self.D, self.page = D, page
+        self.cache = torch.full(m.muse_cache_shape(n, Hkv, page, D, Dv), fill, dtype=torch.uint8,
+                                device="cuda")
+        self.table_np = rng.permutation(n)[:B * max_pages].reshape(B, max_pages)
+        self.table = ints(self.table_np)
+
+    def values(self):
+        """(K [B,Hkv,T,D], V [B,Hkv,T,Dv]) float64 from the bytes."""
+        c = self.cache.cpu().numpy()
+        n, Hkv, per, size = c.shape
+        out = []
+        for x in so.read_tiles(c.reshape(-1, size), self.D):
+            x = x.reshape(n, Hkv, per * 32, -1)[self.table_np]          # [B, mp, Hkv, page, D]
+            x = x.transpose(0, 2, 1, 3, 4)
+            out.append(x.reshape(x.shape[0], Hkv, -1, x.shape[-1]))
+        return out
+
+
+def outliers(seed, *shape, dtype):
+    """Rows with groups of very different sizes, ties and zeros."""
+    x = randn(seed, *shape)
+    x[..., 1::7] *= 30
+    x[..., 32:64] *= 1e-3
+    x[:, :, ::3, :32] = torch.round(x[:, :, ::3, :32] * 2) / 2     # many ties
+    x[:, :, 1::5, 32:64] = 0
+    x[:, :, 2::5, 32:64] *= 1e-38                                   # steps below the normal range
+    x[:, :, 3::5, :32] *= 1e36
+    return x.to(dtype)
+
+
+WIDTHS = [(64, 64), (64, 128), (128, 64), (128, 128)]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("D,Dv", WIDTHS)
+@pytest.mark.parametrize("B,H,N,page,start", [
+    (1, 1, 1, 32, [0]), (2, 3, 1, 64, [31, 32]), (2, 2, 33, 32, [0, 63]), (3, 1, 100, 128, [5, 0, 60]),
+    (1, 4, 257, 256, [1]), (2, 2, 64, 1024, [0, 32])])
+def test_write_then_read_holds_the_rounded_values(B, H, N, page, start, D, Dv, dtype):
+    """The bytes hold exactly what the oracle says, tokens around them stay, and reading gives
+    each value rounded once to its type."""
+    mp = -(-(max(start) + N) // page) + 1
+    s = Store(B, H, page, mp, D, Dv, seed=N, fill=0x5a)
+    before = [x.copy() for x in s.values()]
+    K, V = outliers(1, B, H, N, D, dtype=dtype), outliers(2, B, H, N, Dv, dtype=dtype)
+    m.muse_cache_write(s.cache, K, V, s.table, ints(start))
+    got = s.values()
+    want = [so.held(host(K)), so.held(host(V))]
+    for b in range(B):
+        at = slice(start[b], start[b] + N)
+        for g, w, o in zip(got, want, before):
+            assert np.array_equal(g[b, :, at], w[b])
+            assert np.array_equal(np.delete(g[b], np.r_[at], 1), np.delete(o[b], np.r_[at], 1),
+                                  equal_nan=True)
+    for t, w in zip(m.muse_cache_read(s.cache, s.table, ints(start), N, D, dtype=dtype), want):
+        r = torch.tensor(w).to(F32).to(dtype)     # code * step is exact in float32
+        assert torch.equal(t.cpu(), r)
+    ok()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_infinities_and_nan_stay_in_their_group(dtype):
+    s = Store(1, 1, 32, 2, 128, 64)
+    K, V = randn(1, 1, 1, 40, 128, dtype=dtype), randn(2, 1, 1, 40, 64, dtype=dtype)
+    K[0, 0, 3, 40], K[0, 0, 7, 100], V[0, 0, 9, 2] = float("nan"), float("-inf"), float("inf")
+    m.muse_cache_write(s.cache, K, V, s.table, ints([0]))
+    k, v = m.muse_cache_read(s.cache, s.table, ints([0]), 40, 128, dtype=F32)
+    for t, w in ((k, so.held(host(K))), (v, so.held(host(V)))):
+        assert np.array_equal(host(t), w, equal_nan=True)
+    assert int(torch.isnan(k).sum()) == 64 and int(torch.isnan(v).sum()) == 32
+    ok()
+
+
+def test_counts_strides_and_rows_left_as_they_were():
+    """Ragged counts, [B,N,H,D] memory, a broadcast head; rows past a count neither written nor
+    read."""
+    B, H, N, D, page = 3, 2, 21, 64, 32
+    s = Store(B, H, page, 3, D, D)
+    empty = s.cache.clone()
+    X = randn(3, B, N, H, 2 * D, dtype=BF16)
+    K, V = X[..., :D].transpose(1, 2), X[..., D:].transpose(1, 2)
+    counts, start = [0, 21, 9], [4, 40, 30]
+    m.muse_cache_write(s.cache, K, V, s.table, ints(start), ints(counts))
+    got = s.values()
+    for g, x in zip(got, (K, V)):
+        w = so.held(host(x))
+        for b in range(B):
+            assert np.array_equal(g[b, :, start[b]:start[b] + counts[b]], w[b, :, :counts[b]])
+            rest = np.delete(g[b], np.r_[start[b]:start[b] + counts[b]], 1)
+            assert (rest == 0).all()
+    out = torch.full((2, B, N, H, D), 7.0, dtype=BF16, device="cuda")
+    ko, vo = out[0].transpose(1, 2), out[1].transpose(1, 2)
+    m.muse_cache_read(s.cache, s.table, ints(start), N, D, counts=ints(counts), out=(ko, vo))
+    for t, x in ((ko, K), (vo, V)):
+        w = torch.tensor(so.held(host(x))).to(BF16)
+        for b in range(B):
+            assert torch.equal(t[b, :, :counts[b]].cpu(), w[b, :, :counts[b]])
+            assert (t[b, :, counts[b]:] == 7).all()
+    ok()
+    s.cache.copy_(empty)
+    one = K[:, :1].expand(B, H, N, D)
+    m.muse_cache_write(s.cache, one, one, s.table, ints([0] * B))
+    assert np.array_equal(s.values()[1][:, :, :N], so.held(host(one)))
+
+
+@pytest.mark.parametrize("what", ["page", "negative page", "past the table", "negative start",
+                                  "far start", "count", "negative count"])
+def test_bad_pages_and_positions_are_left_out_and_reported(what):
+    B, H, N, D, page = 2, 1, 40, 64, 32
+    s = Store(B, H, page, 3, D, D)
+    K = randn(1, B, H, N, D, dtype=BF16)
+    start, counts, good = [0, 10], None, np.ones((B, N), bool)
+    tab = s.table_np.copy()
+    if what == "page":
+        tab[0, 1] = len(s.cache)
+        good[0, 32:] = False
+    elif what == "negative page":
+        tab[0, 0] = -1
+        good[0, :32] = False
+    elif what == "past the table":
+        start = [80, 10]
+        good[0, 16:] = False
+    elif what == "negative start":
+        start = [-7, 10]
+        good[0, :7] = False
+    elif what == "far start":
+        start = [2 ** 31 - 8, 10]
+        good[0] = False
+    else:
+        counts = [41 if what == "count" else -1, 40]
+        good[0] = what == "count"
+    table, cnt = ints(tab), None if counts is None else ints(counts)
+    m.muse_cache_write(s.cache, K, K, table, ints(start), cnt)
+    assert m.muse_last_device_status() == 7
+    want = so.held(host(K))
+    for x in s.values():
+        for b in range(B):
+            for n in np.flatnonzero(good[b]):
+                assert np.array_equal(x[b, :, start[b] + n], want[b, :, n])
+    assert int((s.cache != 0).any(-1).sum()) > 0
+    out = torch.full((2, B, H, N, D), 3.0, device="cuda")
+    m.muse_cache_read(s.cache, table, ints(start), N, D, counts=cnt, out=(out[0], out[1]))
+    assert m.muse_last_device_status() == 7
+    for x in out:
+        for b in range(B):
+            assert np.array_equal(host(x[b])[:, good[b]], want[b][:, good[b]])
+            assert (host(x[b])[:, ~good[b]] == 3).all()
+    ok()
+
+
+# -------------------------------------------------------------------- attention over it
+
+def attend_close(got, lse, Q, s, lens, counts, scale, dtype):
+    """A logit is a sum of 16-channel products and four scaled groups in float32: at most 20
+    roundings (2u each where a matrix instruction cuts instead of rounding) of the partial sums,
+    all below X = s sum|q k|, and a query of 22 bits; exp adds 2 steps of its result and the
+    rounding of its argument.  So p is off by a factor of (1 + e), e = (42 u) X + 4 u and the
+    normaliser by as much; products p * step enter in 11 bits (bfloat16 rows) or 22 (float32);
+    their sums, over the tiles of a split, lose 2u a step of 16 tokens."""
+    K, V = s.values()
+    ref, ref_lse, A, X = so.cache_attend(host(Q), K, V, lens, counts, scale)
+    T = max(lens)
+    e = (42 * U * X + 4 * U)[..., None]
+    p = 2.0 ** -11 if dtype == BF16 else 2.0 ** -21
+    tol = HALF[dtype] * np.abs(ref) + A * (2 * e + p + 2 * U * (T / 16 + 40))
+    for b in range(Q.shape[0]):
+        c = counts[b]
+        d = np.abs(got[b, :, :c] - ref[b, :, :c])
+        assert (d <= tol[b, :, :c]).all(), (b, float((d / (tol[b, :, :c] + 1e-300)).max()))
+        r = ref_lse[b, :, :c]
+        live = np.isfinite(r)
+        assert np.array_equal(np.isneginf(lse[b, :, :c]), np.isneginf(r))
+        t = (42 * U * X[b, :, :c] + 4 * U + 4 * U * np.abs(np.where(live, r, 0)) + 2 * U * (T / 16 + 40))
+        assert (np.abs(lse[b, :, :c] - r)[live] <= t[live]).all()
+
+
+def filled(B, Hkv, page, mp, D, Dv, T, dtype=BF16, seed=0, fill=0xff):
+    s = Store(B, Hkv, page, mp, D, Dv, seed=seed, fill=fill)   # 0xff: NaN steps where unwritten
+    if T:
+        K, V = randn(seed + 1, B, Hkv, T, D), randn(seed + 2, B, Hkv, T, Dv)
+        m.muse_cache_write(s.cache, K, V, s.table, ints([0] * B))
+    return s
+
+
+ATTEND = [  # B, H, Hkv, M, page, lens
+    (1, 1, 1, 1, 32, [1]),
+    (1, 8, 8, 1, 64, [33]),
+    (4, 8, 2, 1, 64, [0, 1, 32, 200]),
+    (2, 16, 1, 1, 128, [31, 129]),
+    (3, 5, 1, 1, 32, [64, 65, 63]),
+    (2, 4, 2, 3, 64, [2, 100]),          # a row that sees nothing
+    (2, 10, 2, 7, 32, [300, 7]),
+    (1, 40, 1, 1, 256, [500]),
+    (2, 2, 1, 16, 64, [16, 90]),
+    (1, 4, 2, 33, 64, [70]),
+    (2, 8, 1, 128, 128, [128, 300]),
+    (1, 3, 3, 65, 32, [40]),
+    (1, 1, 1, 1, 1024, [5000]),
+    (40, 2, 2, 1, 32, [(37 * i) % 257 for i in range(40)]),
+]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("D,Dv", WIDTHS)
+@pytest.mark.parametrize("B,H,Hkv,M,page,lens", ATTEND)
+def test_attend_matches_oracle(B, H, Hkv, M, page, lens, D, Dv, dtype):
+    s = filled(B, Hkv, page, -(-max(lens) // page), D, Dv, max(lens))
+    Q = randn(9, B, H, M, D, dtype=dtype)
+    out, lse = m.muse_cache_attend(Q, s.cache, s.table, ints(lens), scale=D ** -0.5)
+    attend_close(host(out), host(lse), Q, s, lens, [M] * B, D ** -0.5, dtype)
+    ok()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("scale", [1.0, -0.3, 0.0, 4.0])
+def test_attend_scales_and_sharp_softmax(scale, dtype):
+    s = filled(2, 2, 64, 8, 64, 64, 450)
+    Q = randn(3, 2, 8, 2, 64, dtype=dtype)
+    out, lse = m.muse_cache_attend(Q, s.cache, s.table, ints([450, 77]), scale=scale)
+    attend_close(host(out), host(lse), Q, s, [450, 77], [2, 2], scale, dtype)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_attend_rows_of_very_different_sizes(dtype):
+    """Queries and values from 1e-12 to 1e12, channels that are a thousand times the others', and
+    values whose steps grow or fall along the sequence."""
+    B, Hkv, T, D = 4, 1, 700, 64
+    s = Store(B, Hkv, 64, 11, D, D)
+    K, V = randn(1, B, Hkv, T, D), randn(2, B, Hkv, T, D)
+    K[..., 5] *= 300
+    ramp = 10.0 ** torch.linspace(-4, 4, T, device="cuda")[:, None]
+    V[0] *= ramp
+    V[1] *= ramp.flip(0)
+    V[2] *= 1e-30
+    V[3, ..., :32] *= 1e12
+    m.muse_cache_write(s.cache, K, V, s.table, ints([0] * B))
+    Q = randn(3, B, 4, 2, D)
+    Q[..., 5] *= 1e-2
+    Q[:, 1] *= 1e-12
+    Q[:, 2] *= 1e-3
+    out, lse = m.muse_cache_attend(Q.to(dtype), s.cache, s.table, ints([T] * B), scale=0.3)
+    attend_close(host(out), host(lse), Q.to(dtype), s, [T] * B, [2] * B, 0.3, dtype)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_attend_a_large_value_that_the_softmax_ignores(dtype):
+    """One token's values are 2^k times the others' and its logit far below: what the others
+    give has to survive, whatever k."""
+    D, T = 64, 70
+    for k in (10, 20, 30, 60):
+        s = Store(1, 1, 64, 2, D, D)
+        K, V = randn(1, 1, 1, T, D) * 0.1, randn(2, 1, 1, T, D)
+        Q = torch.ones(1, 1, 1, D, device="cuda", dtype=dtype)
+        K[0, 0, 33] = -400.0
+        V[0, 0, 33] *= 2.0 ** k
+        m.muse_cache_write(s.cache, K, V, s.table, ints([0]))
+        out, lse = m.muse_cache_attend(Q, s.cache, s.table, ints([T]), scale=1.0)
+        attend_close(host(out), host(lse), Q, s, [T], [1], 1.0, dtype)
+
+
+@pytest.mark.parametrize("M,H", [(1, 4), (6, 4), (40, 8)])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_attend_counts_strides_and_rows_left_as_they_were(M, H, dtype):
+    B, Hkv, D, Dv = 3, 2, 128, 64
+    lens, counts = [90, 3, 41], [M, 0, max(1, M // 2)]
+    s = filled(B, Hkv, 32, 3, D, Dv, 90)
+    X = randn(4, B, M, H, D + 64, dtype=dtype)
+    Q = X[..., :D].transpose(1, 2)
+    out = torch.full((B, M, H, Dv), 5.0, dtype=dtype, device="cuda").transpose(1, 2)
+    lse = torch.full((B, H, M), 5.0, device="cuda")
+    ws = torch.full((m.muse_workspace_size("muse_cache_attend", m.dims(Q, out), Hkv),), 0xff,
+                    dtype=torch.uint8, device="cuda")
+    m.muse_cache_attend(Q, s.cache, s.table, ints(lens), ints(counts), 0.1, out, lse, ws)
+    attend_close(host(out), host(lse), Q, s, lens, counts, 0.1, dtype)
+    for b in range(B):
+        assert (out[b, :, counts[b]:] == 5).all() and (lse[b, :, counts[b]:] == 5).all()
+    ok()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_attend_nan_reaches_only_rows_and_groups_that_see_it(dtype):
+    D, T = 64, 100
+    s = Store(2, 1, 32, 4, D, 128, fill=0xff)
+    K, V = randn(1, 2, 1, T, D), randn(2, 2, 1, T, 128)
+    V[0, 0, 50, 70] = float("inf")       # group 2 of token 50
+    K[1, 0, 97, 3] = float("nan")        # token 97: the last rows see it
+    m.muse_cache_write(s.cache, K, V, s.table, ints([0, 0]))
+    Q = randn(3, 2, 2, 5, D, dtype=dtype)
+    out, lse = m.muse_cache_attend(Q, s.cache, s.table, ints([T, T]), scale=0.1)
+    bad = torch.isnan(out)
+    assert bad[0, :, :, 64:96].all() and not bad[0, :, :, :64].any() and not bad[0, :, :, 96:].any()
+    assert not bad[1, :, :2].any() and bad[1, :, 2:].all()
+    assert torch.isfinite(lse[0]).all() and torch.isfinite(lse[1, :, :2]).all()
+    assert torch.isnan(lse[1, :, 2:]).all()
+    Q[0, 1, 2, 7] = float("nan")         # a query: its row alone
+    out, lse = m.muse_cache_attend(Q, s.cache, s.table, ints([40, 40]), scale=0.1)
+    bad = torch.isnan(out).all(-1)
+    assert bad.sum() == 1 and bad[0, 1, 2] and torch.isnan(lse).sum() == 1
+    ok()
+
+
+@pytest.mark.parametrize("what", ["page", "long", "negative"])
+@pytest.mark.parametrize("M", [1, 20])
+def test_attend_bad_pages_and_lengths_are_left_out_and_reported(what, M):
+    D = 64
+    s = filled(2, 1, 32, 4, D, D, 128)
+    tab, lens, seen = s.table_np.copy(), [100, 128], [np.arange(100), np.arange(128)]
+    if what == "page":
+        tab[0, 1] = 1 << 20
+        seen[0] = np.delete(seen[0], np.r_[32:64])
+    elif what == "long":
+        lens[0], seen[0] = 1 << 30, np.arange(128)
+    else:
+        lens[0], seen[0] = -5, np.arange(0)
+    Q = randn(3, 2, 2, M, D)
+    out, lse = m.muse_cache_attend(Q, s.cache, ints(tab), ints(lens), scale=0.1)
+    assert m.muse_last_device_status() == 7
+    K, V = s.values()
+    eff = [min(max(l, 0), 128) for l in lens]
+    for b in range(2):
+        for mm in (0, M - 1):
+            see = seen[b][seen[b] < eff[b] - M + mm + 1]
+            ref, rl, A, X = so.cache_attend(host(Q)[b:b + 1, :, mm:mm + 1], [K[b][:, see]],
+                                            [V[b][:, see]], [len(see)], [1], 0.1)
+            assert np.allclose(host(out)[b:b + 1, :, mm:mm + 1], ref, atol=1e-5)
+            assert np.allclose(host(lse)[b:b + 1, :, mm:mm + 1], rl, atol=1e-5)
+    ok()
+
+
+def test_attend_repeats_exactly_and_does_not_depend_on_the_workspace():
+    s = filled(3, 2, 64, 32, 64, 64, 2000)
+    Q = randn(1, 3, 8, 1, 64, dtype=BF16)
+    lens = ints([2000, 17, 1234])
+    n = m.muse_workspace_size("muse_cache_attend", m.dims(Q), 2)
+    ref = None
+    for fill in (0, 0xff, 0x7f):
+        ws = torch.full((n,), fill, dtype=torch.uint8, device="cuda")
+        out = m.muse_cache_attend(Q, s.cache, s.table, lens, scale=0.125, ws=ws)
+        ref = ref or [x.clone() for x in out]
+        assert all(torch.equal(a, b) for a, b in zip(out, ref))
+
+
+def test_one_sequence_alone_and_in_a_batch():
+    """A sequence's answer agrees with the same sequence answered alone, to float32 rounding of
+    another split (A <= max|v| ~ 5: 1e-5 covers 2u (T / 16 + 40) A twice)."""
+    s = filled(5, 1, 64, 20, 128, 128, 1200)
+    Q = randn(1, 5, 8, 1, 128)
+    lens = [1200, 900, 33, 0, 1]
+    out, lse = m.muse_cache_attend(Q, s.cache, s.table, ints(lens), scale=0.1)
+    for b in range(5):
+        o, l = m.muse_cache_attend(Q[b:b + 1], s.cache, s.table[b:b + 1], ints(lens[b:b + 1]), scale=0.1)
+        assert torch.allclose(o[0], out[b], atol=2e-4, rtol=0) and torch.allclose(l[0], lse[b], atol=1e-5, rtol=0)
+
+
+# ------------------------------------------------------------------ together, streams, graphs
+
+def test_a_prompt_and_the_tokens_after_it():
+    """As they are used: positions into Q and K, MuSe over the prompt, its keys and values into
+    the cache, then tokens one by one; every answer is exact attention over what the cache
+    holds."""
+    B, H, N, D, block, page = 2, 4, 256, 64, 128, 64
+    sec = (8, 12, 12)
+    Q, K, V = (randn(i, B, H, N, D, dtype=BF16) * 0.3 for i in range(3))
+    pos = ints(np.arange(N)[None, None].repeat(3, 1).repeat(B, 0))
+    Qr, Kr = m.muse_rope_axes(Q, pos, sec, K=K)
+    O = m.muse_causal_blocks(Qr, Kr, V, block, 16, 16, 3, scale=D ** -0.5)
+    assert torch.isfinite(O).all()
+    s = Store(B, H, page, N // page + 1, D, D)
+    m.muse_cache_write(s.cache, Kr, V, s.table, ints([0] * B))
+    # the cache's own prompt rows through MuSe: what later tokens see
+    Kc, Vc = m.muse_cache_read(s.cache, s.table, ints([0] * B), N, D)
+    assert torch.isfinite(m.muse_causal_blocks(Qr, Kc, Vc, block, 16, 16, 3, scale=D ** -0.5)).all()
+    for t in range(3):
+        q, k, v = (randn(10 + 3 * t + i, B, H, 1, D, dtype=BF16) * 0.3 for i in range(3))
+        at = ints(np.full((B, 3, 1), N + t))
+        q, k = m.muse_rope_axes(q, at, sec, K=k)
+        m.muse_cache_write(s.cache, k, v, s.table, ints([N + t] * B))
+        out, lse = m.muse_cache_attend(q, s.cache, s.table, ints([N + t + 1] * B), scale=D ** -0.5)
+        attend_close(host(out), host(lse), q, s, [N + t + 1] * B, [1] * B, D ** -0.5, BF16)
+    ok()
+
+
+def test_replayed_steps_in_a_graph_follow_the_lengths():
+    """A captured step (positions, write, attend) replayed with lengths, positions and rows
+    updated in place; two graphs share one workspace."""
+    B, H, Hkv, D, page = 3, 8, 2, 64, 32
+    s = filled(B, Hkv, page, 8, D, D, 200, fill=0)
+    q, k, v = (randn(i, B, h, 1, D, dtype=BF16) for i, h in ((1, H), (2, Hkv), (3, Hkv)))
+    lens0 = np.array([199, 0, 63])
+    pos, start, lens = ints(lens0[:, None, None]), ints(lens0), ints(lens0 + 1)
+    out, lse = torch.empty_like(q), torch.empty(B, H, 1, device="cuda")
+    qr, kr = torch.empty_like(q), torch.empty_like(k)
+    ws = m.workspace("muse_cache_attend", m.dims(q), Hkv)
+
+    def step():
+        m.muse_rope_axes(q, pos, [32], K=k, out=qr, k_out=kr)
+        m.muse_cache_write(s.cache, kr, v, s.table, start)
+        m.muse_cache_attend(qr, s.cache, s.table, lens, scale=0.125, out=out, lse=lse, ws=ws)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graphs = []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            step()
+        graphs.append(g)
+    for i in range(5):
+        now = lens0 + i + 1
+        pos.copy_(ints(now[:, None, None]))
+        start.copy_(ints(now))
+        lens.copy_(ints(now + 1))
+        for j, x in enumerate((q, k, v)):
+            x.copy_(randn(100 * i + j, *x.shape, dtype=BF16))
+        graphs[i % 2].replay()
+        attend_close(host(out), host(lse), qr, s, (now + 1).tolist(), [1] * B, 0.125, BF16)
+    ok()
+
+
+def test_calls_on_two_streams_at_once():
+    s = filled(2, 2, 64, 32, 128, 128, 2000)
+    Qs = [randn(i, 2, 16, 1, 128, dtype=BF16) for i in range(6)]
+    lens = ints([2000, 1500])
+    ref = [m.muse_cache_attend(q, s.cache, s.table, lens, scale=0.09)[0].clone() for q in Qs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = []
+    for i, q in enumerate(Qs * 4):
+        with torch.cuda.stream(streams[i % 2]):
+            got.append(m.muse_cache_attend(q, s.cache, s.table, lens, scale=0.09)[0])
+    torch.cuda.synchronize()
+    for i, o in enumerate(got):
+        assert torch.equal(o, ref[i % 6])
+    ok()
+
+
+def test_launch_counter_counts_the_serving_kernels():
+    lib = m.lib()
+    lib.muse_launch_counter.restype = m.ctypes.c_uint64
+    s = filled(1, 1, 32, 2, 64, 64, 40)
+    Q = randn(1, 1, 1, 1, 64)
+    n0 = lib.muse_launch_counter()
+    m.muse_rope_axes(Q, ints([[5]]), [32])
+    m.muse_cache_read(s.cache, s.table, ints([0]), 40, 64)
+    m.muse_cache_attend(Q, s.cache, s.table, ints([40]))
+    assert lib.muse_launch_counter() - n0 >= 3
