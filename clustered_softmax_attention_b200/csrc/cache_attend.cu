@@ -1,129 +1,886 @@
 // Causal attention of a sequence's newest rows over its 4-bit cache.
+//
+// The rows of one cache head (the H / Hkv query heads of every new token) are the columns of a
+// 16 x 8 matrix-instruction tile and tokens, then value channels, its rows, so that eight rows
+// or fewer (a token of grouped heads) fill it.  Keys and values enter as their integer codes,
+// dequantised in registers to signed float16 (exact, two codes a register):
+//   S^T = sum_w kstep[t][w] (sum_{c in group w} code_tc q_c),    p = 2^(S rf - m),
+//   O^T = sum_t code_tc (p_t vstep[t][w]),
+// so a step multiplies a sum (keys) or a weight (values), never a code.  The layout of a tile is
+// such that 16 bytes a lane are operands as they lie; only the weights are turned over between
+// the two products, eight by eight (movmatrix).
+//
+// Work is split evenly whatever the lengths: the 32-token tiles of all (sequence, head, row
+// block) items form one line, and every CTA takes a stretch of it.  An item that lies in one
+// stretch is finished there; the others leave float32 partial sums (at most two a CTA), which
+// attend_join adds in the order of the CTAs: results do not depend on timing.
+#include <algorithm>
+#include <atomic>
+
+#include <cuda_fp16.h>
+
 #include "cache.cuh"
 
 namespace muse {
 namespace {
 
+constexpr int kMaxCtas = 592;   // 148 SMs x 4: the bound of the partials in the workspace
+constexpr int kWarps = 4;
 struct AttendArgs {
   muse_rows Q, O;
   float *lse;
   const int32_t *lens, *counts;
-  int B, H, M;
+  int B, H, M, G;      // G = H / Hkv
+  int nrb;             // row blocks of an item's G * M rows
+  int min_tiles;       // a CTA takes at least so many
   float scale;
+  float *part;         // [2 kMaxCtas][rows of a block][Dv]
+  float *part_ml;      // [2 kMaxCtas][rows of a block][2]
 };
 
-// One CTA per row (b, h, m); its four warps take tiles in turn, a lane a token for the logits
-// and a channel of every group for the values.
-template <typename T, int D, int Dv>
-__global__ void __launch_bounds__(128) attend_rows(const AttendArgs a, const CacheView v,
-                                                   int *status) {
-  using S = TileShape<D, Dv>;
-  constexpr int NGk = D / 32, NG = Dv / 32;
-  __shared__ float q[D];
-  __shared__ float sm[4], sl[4], so[4][Dv];
-  const int m = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int count = row_count(a.counts, b, a.M, status);
-  if (m >= count) return;
-  int len = a.lens[b];
+// New rows, and tokens that the last of them may see, of sequence b.
+__device__ __forceinline__ int seq_rows(const AttendArgs &a, int b) {
+  if (!a.counts) return a.M;
+  return min(max(a.counts[b], 0), a.M);
+}
+__device__ __forceinline__ int seq_len(const AttendArgs &a, const CacheView &v, int b) {
   const int64_t cap = (int64_t)v.max_pages << v.page_log2;
-  if ((len < 0 || len > cap) && tid == 0) report(status, MUSE_ERR_DEVICE);
-  len = (int)min((int64_t)max(len, 0), cap);
-  const int see = max(0, len - count + m + 1);
-  const int hk = h / (a.H / v.Hkv);
-  if (tid < D)
-    q[tid] = ld_elem((const T *)a.Q.p + b * a.Q.sb + h * a.Q.sh + m * a.Q.sn + tid) * a.scale;
+  return (int)min((int64_t)max(a.lens[b], 0), cap);
+}
+__device__ __forceinline__ int seq_tiles(const AttendArgs &a, const CacheView &v, int b) {
+  return seq_rows(a, b) ? (seq_len(a, v, b) + kTile - 1) / kTile : 0;
+}
+
+// The line of tiles: its length, and the sequence in which position x lies with the position
+// of that sequence's first tile.  Each thread sums a run of sequences.
+struct Line {
+  int64_t total, first;
+  int b;
+};
+template <int kThreads>
+__device__ __forceinline__ int64_t line_total(const AttendArgs &a, const CacheView &v, int64_t *run) {
+  const int tid = threadIdx.x, per = (a.B + kThreads - 1) / kThreads;
+  const int b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
+  int64_t s = 0;
+  for (int b = b0; b < b1; ++b) s += seq_tiles(a, v, b);
+  // inclusive scan over the threads
+  const int lane = tid & 31, warp = tid >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, s, o);
+    if (lane >= o) s += y;
+  }
+  if (lane == 31) run[kThreads + warp] = s;
   __syncthreads();
-  float mx = -CUDART_INF_F, l = 0.f, o[NG];
+  int64_t add = 0;
+  for (int w = 0; w < warp; ++w) add += run[kThreads + w];
+  run[tid] = (s + add) * v.Hkv * a.nrb;
+  __syncthreads();
+  return run[kThreads - 1];
+}
+template <int kThreads>
+__device__ __forceinline__ void line_find(const AttendArgs &a, const CacheView &v,
+                                          const int64_t *run, int64_t x, int &b, int64_t &first) {
+  int lo = 0, hi = kThreads - 1;  // the first thread whose run ends behind x
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (run[mid] > x) hi = mid;
+    else lo = mid + 1;
+  }
+  const int per = (a.B + kThreads - 1) / kThreads;
+  b = lo * per;
+  first = lo ? run[lo - 1] : 0;
+  while (b < a.B - 1) {
+    const int64_t n = (int64_t)seq_tiles(a, v, b) * v.Hkv * a.nrb;
+    if (first + n > x) break;
+    first += n;
+    ++b;
+  }
+}
+__device__ __forceinline__ int64_t stretch(int64_t total, int ctas, int min_tiles) {
+  return max((int64_t)min_tiles, (total + ctas - 1) / ctas);
+}
+
+// ------------------------------------------------------------------ small device pieces
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void slice_sync(int slice) {  // the N warps of a token slice
+  if (N == 1) __syncwarp();
+  else asm volatile("bar.sync %0, %1;" ::"r"(1 + slice), "n"(32 * N) : "memory");
+}
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                        uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// An 8 x 8 matrix of 16-bit values turned over: lane (g, q) gives row g, columns 2 q and 2 q + 1,
+// and takes column g, rows 2 q and 2 q + 1.
+__device__ __forceinline__ uint32_t turned(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t bits(__half2 h) { return *reinterpret_cast<const uint32_t *>(&h); }
+__device__ __forceinline__ uint32_t bits(__nv_bfloat162 h) {
+  return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  return bits(__floats2half2_rn(lo, hi));
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// Four pairs of codes of a word (nibbles n and n + 4) as float16: 1024 + u, or 1024 + 16 u,
+// without its offset.
+__device__ __forceinline__ void codes_f16(uint32_t x, uint32_t (&c)[4]) {
+  const uint32_t y = x >> 8;
+  const __half2 less = __half2half2(__ushort_as_half(0xE408));     // -1032
+  const __half2 part = __half2half2(__ushort_as_half(0x2C00));     // 1/16
+  const __half2 less16 = __half2half2(__ushort_as_half(0xD480));   // -72
+  uint32_t t[4] = {(x & 0x000f000fu) | 0x64006400u, (x & 0x00f000f0u) | 0x64006400u,
+                   (y & 0x000f000fu) | 0x64006400u, (y & 0x00f000f0u) | 0x64006400u};
 #pragma unroll
-  for (int g = 0; g < NG; ++g) o[g] = 0.f;
-  for (int tile = warp; tile * 32 < see; tile += 4) {
-    const uint8_t *p = cache_tile(v, b, hk, tile, S::kBytes);
-    if (!p) {
-      report(status, MUSE_ERR_DEVICE);
-      continue;
-    }
-    const uint32_t *kw = (const uint32_t *)p, *vw = (const uint32_t *)(p + S::kV);
-    const uint16_t *ks = (const uint16_t *)(p + S::kKStep), *vs = (const uint16_t *)(p + S::kVStep);
-    float x = 0.f;
+  for (int i = 0; i < 4; ++i) {
+    const __half2 h = *reinterpret_cast<const __half2 *>(&t[i]);
+    c[i] = bits(i & 1 ? __hfma2(h, part, less16) : __hadd2(h, less));
+  }
+}
+// The same pairs as bfloat16 (128 + u without its offset).
+__device__ __forceinline__ void codes_bf16(uint32_t x, uint32_t (&c)[4]) {
+  const __nv_bfloat162 less = __bfloat162bfloat162(__ushort_as_bfloat16(0xC308));  // -136
 #pragma unroll
-    for (int w = 0; w < NGk; ++w) {
-      float s = 0.f;
-      for (int c = 0; c < 4; ++c) {
-        const uint32_t u = kw[key_word<D>(lane, c, w)];
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t t = ((x >> (4 * i)) & 0x000f000fu) | 0x43004300u;
+    c[i] = bits(__hadd2(*reinterpret_cast<const __nv_bfloat162 *>(&t), less));
+  }
+}
+__device__ __forceinline__ float lo_f(uint32_t x) { return __uint_as_float(x << 16); }
+__device__ __forceinline__ float hi_f(uint32_t x) { return __uint_as_float(x & 0xffff0000u); }
+// Group w of two packed steps.
+template <int N>
+__device__ __forceinline__ float step_of(const uint32_t (&s)[N], int w) {
+  return w & 1 ? hi_f(s[w >> 1]) : lo_f(s[w >> 1]);
+}
+
+// Words of eight tokens: K words of token 8 i + g for the groups, V words of tokens 8 i + 2 q and
+// 8 i + 2 q + 1 for the halves.
+template <int D>
+__device__ __forceinline__ void words(const uint8_t *codes, int i, int lane, uint32_t (&w)[D / 32]) {
+  const uint4 *p = reinterpret_cast<const uint4 *>(codes);
+  if (D == 128) {
+    const uint4 x = p[i * 32 + lane];
+    w[0] = x.x;
+    w[1] = x.y;
+    w[D / 32 - 2] = x.z;
+    w[D / 32 - 1] = x.w;
+  } else {
+    const uint2 x = reinterpret_cast<const uint2 *>(p + (i >> 1) * 32 + lane)[i & 1];
+    w[0] = x.x;
+    w[1] = x.y;
+  }
+}
+// Steps of token t, two groups a register.
+template <int D>
+__device__ __forceinline__ void steps(const uint8_t *p, int t, uint32_t (&s)[D / 64]) {
+  if (D == 128) {
+    const uint2 x = reinterpret_cast<const uint2 *>(p)[t];
+    s[0] = x.x;
+    s[D / 64 - 1] = x.y;
+  } else {
+    s[0] = reinterpret_cast<const uint32_t *>(p)[t];
+  }
+}
+// Both tokens' words of a value group: a half word of each, four channels.
+template <int Dv>
+__device__ __forceinline__ uint32_t value_pair(const uint32_t (&x)[Dv / 32], int grp) {
+  return __byte_perm(Dv == 128 ? x[grp >> 1] : x[0], Dv == 128 ? x[Dv / 64 + (grp >> 1)] : x[1],
+                     grp & 1 ? 0x7632 : 0x5410);
+}
+
+// O^T of 8 NB rows in units of 1 / unit[group]: [rows 8 nb + 2 q + e][channel 16 j + 8 h + g] at
+// [nb][j][2 h + e].
+template <int Dv, int NB>
+struct Acc {
+  float o[NB][Dv / 16][4];
+};
+// Logits, then weights, of the tile: [nb][i][e] = row 8 nb + 2 q + e, token 8 i + g.
+template <int NB>
+struct Tok {
+  float p[NB][4][2];
+};
+// Which tokens of a tile the rows do not see (left = see - the tile's first token).
+template <int NB>
+struct Hide {
+  bool edge;
+  int left[NB][2];
+  __device__ __forceinline__ bool at(int nb, int t, int e) const { return edge && t >= left[nb][e]; }
+};
+
+// O += (p vstep) code with float16 weights; ds: the steps as bfloat16 in the accumulators' unit,
+// between 2 and 2^9.
+template <int Dv, int NB>
+__device__ __forceinline__ void values_f16(Acc<Dv, NB> &acc, const uint8_t *codes,
+                                           const uint32_t (&ds)[4][Dv / 64], const Tok<NB> &tk,
+                                           int lane) {
 #pragma unroll
-        for (int n = 0; n < 8; ++n) s = fmaf(code_value(u, n), q[32 * w + 8 * c + n], s);
+  for (int kk = 0; kk < 2; ++kk) {
+    uint32_t x[2][Dv / 32];
+    words<Dv>(codes, 2 * kk, lane, x[0]);
+    words<Dv>(codes, 2 * kk + 1, lane, x[1]);
+#pragma unroll
+    for (int grp = 0; grp < Dv / 32; ++grp) {
+      uint32_t c[2][4];
+      codes_f16(value_pair<Dv>(x[0], grp), c[0]);
+      codes_f16(value_pair<Dv>(x[1], grp), c[1]);
+      // nibbles n and n + 4 of the pair are channel 8 n + g of the group for both tokens: the
+      // half words hold n = 0..3 each
+      const uint32_t a0[4] = {c[0][0], c[0][1], c[1][0], c[1][1]};
+      const uint32_t a1[4] = {c[0][2], c[0][3], c[1][2], c[1][3]};
+      const float f0 = step_of(ds[2 * kk], grp), f1 = step_of(ds[2 * kk + 1], grp);
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
+        const float(&p)[4][2] = tk.p[nb];
+        const uint32_t b0 = turned(pack_f16(p[2 * kk][0] * f0, p[2 * kk][1] * f0));
+        const uint32_t b1 = turned(pack_f16(p[2 * kk + 1][0] * f1, p[2 * kk + 1][1] * f1));
+        mma_f16(acc.o[nb][2 * grp], a0, b0, b1);
+        mma_f16(acc.o[nb][2 * grp + 1], a1, b0, b1);
       }
-      x = fmaf(s, step_value(ks[lane * NGk + w]), x);
     }
-    if (tile * 32 + lane >= see) x = -CUDART_INF_F;
-    const float top = fmaxf(mx, warp_max(x));
-    const float ref = top == -CUDART_INF_F ? 0.f : top;
-    const float fix = expf(mx - ref), e = expf(x - ref);
-    mx = top;
-    l = l * fix + warp_sum(e);
+  }
+}
+
+// The same with p vstep in PARTS bfloat16 pieces (16 or 24 bits): any range.  The sum over the
+// tile's 32 tokens is formed apart and added once.
+template <int Dv, int NB, int PARTS>
+__device__ __forceinline__ void values_wide(Acc<Dv, NB> &acc, const uint8_t *codes,
+                                            const uint8_t *vstep, const Tok<NB> &tk,
+                                            const float (&unit)[Dv / 32], const Hide<NB> &hide,
+                                            int lane) {
+  const int g = lane >> 2;
 #pragma unroll
-    for (int g = 0; g < NG; ++g) o[g] *= fix;
-    const int live = min(32, see - tile * 32);
-    for (int t = 0; t < live; ++t) {
-      const float pt = __shfl_sync(0xffffffffu, e, t);
+  for (int grp = 0; grp < Dv / 32; ++grp) {
+    float t[NB][2][4];
 #pragma unroll
-      for (int g = 0; g < NG; ++g) {
-        const int c = 32 * g + lane;
-        const uint32_t u = vw[value_word<Dv>(t, c & 7, c >> 6)] >> (4 * ((c & 63) >> 3));
-        o[g] = fmaf(pt * step_value(vs[t * NG + g]), code_value(u, 0), o[g]);
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) t[nb][e >> 2][e & 3] = 0.f;
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk) {
+      uint32_t c[2][4];
+      float f[2];
+#pragma unroll
+      for (int ii = 0; ii < 2; ++ii) {
+        uint32_t x[Dv / 32], s[Dv / 64];
+        words<Dv>(codes, 2 * kk + ii, lane, x);
+        codes_bf16(value_pair<Dv>(x, grp), c[ii]);
+        steps<Dv>(vstep, 8 * (2 * kk + ii) + g, s);
+        f[ii] = step_of(s, grp) * unit[grp];
+      }
+      const uint32_t a0[4] = {c[0][0], c[0][1], c[1][0], c[1][1]};
+      const uint32_t a1[4] = {c[0][2], c[0][3], c[1][2], c[1][3]};
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
+        float w[2][2];
+#pragma unroll
+        for (int ii = 0; ii < 2; ++ii)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int i = 2 * kk + ii;
+            w[ii][e] = hide.at(nb, 8 * i + g, e) ? 0.f : tk.p[nb][i][e] * f[ii];
+          }
+#pragma unroll
+        for (int part = 0; part < PARTS; ++part) {
+          uint32_t b[2];
+#pragma unroll
+          for (int ii = 0; ii < 2; ++ii) {
+            b[ii] = bits(__floats2bfloat162_rn(w[ii][0], w[ii][1]));
+            w[ii][0] -= lo_f(b[ii]);
+            w[ii][1] -= hi_f(b[ii]);
+            b[ii] = turned(b[ii]);
+          }
+          mma_bf16(t[nb][0], a0, b[0], b[1]);
+          mma_bf16(t[nb][1], a1, b[0], b[1]);
+        }
       }
     }
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) acc.o[nb][2 * grp + (e >> 2)][e & 3] += t[nb][e >> 2][e & 3];
+  }
+}
+
+// One CTA: RT row tiles of 8 NB x kWarps / RT token slices.
+template <typename T, int D, int Dv, int NB, int RT>
+struct Shape {
+  static constexpr int kSlices = kWarps / RT;
+  static constexpr int kTileRows = 8 * NB;
+  static constexpr int kRows = kTileRows * RT;
+  static constexpr int kStages = 3;                          // tiles under way of a token slice
+  static constexpr int kRing = kSlices * kStages * TileShape<D, Dv>::kBytes;
+  static constexpr int kSumRow = Dv + 4;                     // so that lanes store to other banks
+  static constexpr int kSum = kSlices * kRows * kSumRow * 4; // the slices' sums, over the ring
+  static constexpr int kSmem = kRing > kSum ? kRing : kSum;
+  static constexpr int kParts = sizeof(T) == 4 ? 2 : 1;      // float16 pieces of a query
+};
+
+template <typename T, int D, int Dv, int NB, int RT>
+__global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 4 ? 2 : NB == 1 ? 4 : 3)
+attend(const AttendArgs a, const CacheView v, int *status) {
+  using S = TileShape<D, Dv>;
+  using C = Shape<T, D, Dv, NB, RT>;
+  constexpr int NGk = D / 32, NG = Dv / 32, TS = C::kSlices, kThreads = 32 * kWarps;
+  constexpr int QP = C::kParts, kStages = C::kStages;
+  constexpr unsigned kAll = 0xffffffffu;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ int64_t run[kThreads + kWarps];
+  __shared__ float s_ml[TS][C::kRows][2];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q = lane & 3;
+  const int rt = warp % RT, ts = warp / RT;
+
+  const int64_t total = line_total<kThreads>(a, v, run);
+  const int64_t per = stretch(total, gridDim.x, a.min_tiles);
+  const int64_t x0 = blockIdx.x * per, x1 = min(total, x0 + per);
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (x0 >= x1) return;
+  int b;
+  int64_t first;
+  line_find<kThreads>(a, v, run, x0, b, first);
+
+  uint8_t *ring = smem + ts * kStages * S::kBytes;
+  const uint32_t ring_s = (uint32_t)__cvta_generic_to_shared(ring);
+  const int slice_tid = rt * 32 + lane;
+
+  int64_t x = x0;
+  int nt = seq_tiles(a, v, b), len = seq_len(a, v, b), rows = seq_rows(a, b);
+  while (x < x1) {
+    // the item of position x, and the part [t0, t1) of its nt tiles in this stretch
+    while (x >= first + (int64_t)nt * v.Hkv * a.nrb) {
+      first += (int64_t)nt * v.Hkv * a.nrb;
+      ++b;
+      nt = seq_tiles(a, v, b);
+      len = seq_len(a, v, b);
+      rows = seq_rows(a, b);
+    }
+    const int item = (int)((x - first) / nt), hk = item / a.nrb, rb = item - hk * a.nrb;
+    const int t0 = (int)((x - first) - (int64_t)item * nt);
+    const int t1 = (int)min((int64_t)nt, t0 + (x1 - x));
+    x += t1 - t0;
+
+    // ---- the slice's tiles t0 + ts, + TS, ...: kStages - 1 of them under way
+    const int n_it = max(0, (t1 - t0 - ts + TS - 1) / TS);
+    uint32_t there = 0;  // stages that hold a tile (a page outside the cache is left out)
+    const uint8_t *src = n_it ? cache_tile(v, b, hk, t0 + ts, S::kBytes) : nullptr;
+    auto fetch = [&](int it) {
+      if (it < n_it) {
+        const int st = it % kStages;
+        if (src) {
+          for (int i = slice_tid; i < S::kBytes / 16; i += 32 * RT)
+            cp16(ring_s + st * S::kBytes + i * 16, src + i * 16);
+          there |= 1u << st;
+        } else {
+          there &= ~(1u << st);
+          if (slice_tid == 0) report(status, MUSE_ERR_DEVICE);
+        }
+        // the next tile's place, asked for a step ahead
+        if (it + 1 < n_it) src = cache_tile(v, b, hk, t0 + ts + (it + 1) * TS, S::kBytes);
+      }
+      cp_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) fetch(i);
+
+    // ---- queries as float16 pieces, a power of two a row: this lane's operand is row g
+    uint32_t qb[QP][NB][D / 16][2];
+    float rf[NB][2];     // rows 2 q + e from here on
+    int see[NB][2], see_all = 0x7fffffff;
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+      const int row0 = rb * C::kRows + rt * C::kTileRows + 8 * nb;
+      const int m = (row0 + g) / a.G, h = hk * a.G + (row0 + g - m * a.G);
+      const T *from = (const T *)a.Q.p + b * a.Q.sb + h * a.Q.sh + m * a.Q.sn;
+      float f[NGk][8], top = 0.f;
+      bool bad = false;
+#pragma unroll
+      for (int w = 0; w < NGk; ++w) {
+        if (m >= rows) {
+#pragma unroll
+          for (int n = 0; n < 8; ++n) f[w][n] = 0.f;
+        } else if (sizeof(T) == 4) {
+          const float4 u0 = *reinterpret_cast<const float4 *>(from + 32 * w + 8 * q);
+          const float4 u1 = *reinterpret_cast<const float4 *>(from + 32 * w + 8 * q + 4);
+          f[w][0] = u0.x; f[w][1] = u0.y; f[w][2] = u0.z; f[w][3] = u0.w;
+          f[w][4] = u1.x; f[w][5] = u1.y; f[w][6] = u1.z; f[w][7] = u1.w;
+        } else {
+          const uint4 u = *reinterpret_cast<const uint4 *>(from + 32 * w + 8 * q);
+          f[w][0] = lo_f(u.x); f[w][1] = hi_f(u.x); f[w][2] = lo_f(u.y); f[w][3] = hi_f(u.y);
+          f[w][4] = lo_f(u.z); f[w][5] = hi_f(u.z); f[w][6] = lo_f(u.w); f[w][7] = hi_f(u.w);
+        }
+#pragma unroll
+        for (int n = 0; n < 8; ++n) {
+          top = fmaxf(top, fabsf(f[w][n]));
+          bad |= !(fabsf(f[w][n]) <= 3.4028235e38f);
+        }
+      }
+      top = fmaxf(top, __shfl_xor_sync(kAll, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(kAll, top, 2));
+      bad = ((__ballot_sync(kAll, bad) >> (4 * g)) & 15u) != 0;
+      // q 2^-e with its largest in [2^14, 2^15): float16 keeps bfloat16 values exactly down to
+      // 2^-31 of the largest, float32 ones to 22 bits in two pieces.  A row with an infinity or a
+      // NaN is NaN.
+      int e = (int)((__float_as_uint(top) >> 23) & 255) - 127 - 14;
+      e = min(max(e, -114), 113);
+      const float mul = bad ? CUDART_NAN_F : a.scale < 0.f ? -ldexpf(1.f, -e) : ldexpf(1.f, -e);
+      // logits in units of log 2
+      const float rfg = fmaxf(ldexpf(fabsf(a.scale) * 1.44269504f, e), 1e-37f);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        rf[nb][k] = __shfl_sync(kAll, rfg, (2 * q + k) * 4);
+        const int mm = (row0 + 2 * q + k) / a.G;
+        see[nb][k] = mm < rows ? min(max(len - rows + mm + 1, 0), len) : 0;
+        see_all = min(see_all, see[nb][k]);
+      }
+#pragma unroll
+      for (int w = 0; w < NGk; ++w) {
+        float hi[8], lo[8];
+#pragma unroll
+        for (int n = 0; n < 8; ++n) {
+          const float u = f[w][n] * mul;
+          hi[n] = __half2float(__float2half_rn(u));
+          lo[n] = (u - hi[n]) * 2048.f;
+        }
+        // the two halves of a register of codes are nibbles n and n + 4
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          qb[0][nb][2 * w + k][0] = pack_f16(hi[2 * k], hi[2 * k + 4]);
+          qb[0][nb][2 * w + k][1] = pack_f16(hi[2 * k + 1], hi[2 * k + 5]);
+          if (QP == 2) {
+            qb[QP - 1][nb][2 * w + k][0] = pack_f16(lo[2 * k], lo[2 * k + 4]);
+            qb[QP - 1][nb][2 * w + k][1] = pack_f16(lo[2 * k + 1], lo[2 * k + 5]);
+          }
+        }
+      }
+    }
+    // tokens that every row of the warp's tile sees
+    see_all = min(see_all, __shfl_xor_sync(kAll, see_all, 1));
+    see_all = min(see_all, __shfl_xor_sync(kAll, see_all, 2));
+
+    Acc<Dv, NB> acc;
+    float mx[NB][2], l[NB][2];
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+      for (int e = 0; e < Dv / 4; ++e) acc.o[nb][e >> 2][e & 3] = 0.f;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        mx[nb][e] = -CUDART_INF_F;
+        l[nb][e] = 0.f;
+      }
+    }
+    // the accumulators of value group w hold O * unit[w], a power of two; shift: what takes two
+    // groups' steps, as bits, to that unit
+    uint32_t shift[NG / 2];
+    float unit[NG];
+    bool have_unit = false;
+
+    for (int it = 0; it < n_it; ++it) {
+      cp_wait<kStages - 2>();
+      slice_sync<RT>(ts);
+      const bool here = (there >> (it % kStages)) & 1u;
+      fetch(it + kStages - 1);
+      if (!here) continue;
+      const uint8_t *tile = ring + (it % kStages) * S::kBytes;
+      const int tok = (t0 + ts + it * TS) * kTile;
+
+      // ---- logits
+      Tok<NB> tk;
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt) {
+        uint32_t w[2][NGk], ks[2][NGk / 2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          words<D>(tile + S::kK, 2 * mt + h, lane, w[h]);
+          steps<D>(tile + S::kKStep, 16 * mt + 8 * h + g, ks[h]);
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) tk.p[nb][2 * mt + h][0] = tk.p[nb][2 * mt + h][1] = 0.f;
+        }
+#pragma unroll
+        for (int c = 0; c < NGk; ++c) {
+          uint32_t k[2][4];
+          codes_f16(w[0][c], k[0]);
+          codes_f16(w[1][c], k[1]);
+          const uint32_t a0[4] = {k[0][0], k[1][0], k[0][1], k[1][1]};
+          const uint32_t a1[4] = {k[0][2], k[1][2], k[0][3], k[1][3]};
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) {
+            float d[4] = {0.f, 0.f, 0.f, 0.f};
+            mma_f16(d, a0, qb[0][nb][2 * c][0], qb[0][nb][2 * c][1]);
+            mma_f16(d, a1, qb[0][nb][2 * c + 1][0], qb[0][nb][2 * c + 1][1]);
+            if (QP == 2) {
+              float d2[4] = {0.f, 0.f, 0.f, 0.f};
+              mma_f16(d2, a0, qb[QP - 1][nb][2 * c][0], qb[QP - 1][nb][2 * c][1]);
+              mma_f16(d2, a1, qb[QP - 1][nb][2 * c + 1][0], qb[QP - 1][nb][2 * c + 1][1]);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) d[e] = fmaf(d2[e], 1.f / 2048.f, d[e]);
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const float f = step_of(ks[h], c);
+              float(&p)[2] = tk.p[nb][2 * mt + h];
+              p[0] = fmaf(d[2 * h], f, p[0]);
+              p[1] = fmaf(d[2 * h + 1], f, p[1]);
+            }
+          }
+        }
+      }
+      Hide<NB> hide;
+      hide.edge = tok + kTile > see_all;
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) hide.left[nb][e] = see[nb][e] - tok;
+      if (hide.edge) {
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              if (hide.at(nb, 8 * i + g, e)) tk.p[nb][i][e] = -CUDART_INF_F;
+      }
+      // ---- softmax: the running maximum is a reference, and moves when a weight would pass 2^6
+      float top[NB][2];
+      bool move = false;
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float(&p)[4][2] = tk.p[nb];
+          float y = fmaxf(fmaxf(p[0][e], p[1][e]), fmaxf(p[2][e], p[3][e]));
+          y = fmaxf(y, __shfl_xor_sync(kAll, y, 4));
+          y = fmaxf(y, __shfl_xor_sync(kAll, y, 8));
+          y = fmaxf(y, __shfl_xor_sync(kAll, y, 16));
+          top[nb][e] = y * rf[nb][e];
+          move |= top[nb][e] > mx[nb][e] + 6.f;
+        }
+      if (__any_sync(kAll, move)) {
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float now = fmaxf(mx[nb][e], top[nb][e]);
+            const float fix = now == -CUDART_INF_F ? 1.f : ex2(mx[nb][e] - now);
+            mx[nb][e] = now;
+            l[nb][e] *= fix;
+#pragma unroll
+            for (int j = 0; j < Dv / 16; ++j) {
+              acc.o[nb][j][e] *= fix;
+              acc.o[nb][j][2 + e] *= fix;
+            }
+          }
+      }
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float &y = tk.p[nb][i][e];
+            y = ex2(fmaf(y, rf[nb][e], -mx[nb][e]));
+            if (hide.at(nb, 8 * i + g, e)) y = 0.f;
+            l[nb][e] += y;
+          }
+
+      // ---- value steps in the unit of the accumulators, which the first tile sets: its largest
+      // step comes to [2^5, 2^6)
+      uint32_t ds[4][NG / 2];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) steps<Dv>(tile + S::kVStep, 8 * i + g, ds[i]);
+      if (!have_unit) {
+        have_unit = true;
+#pragma unroll
+        for (int w = 0; w < NG / 2; ++w) {
+          uint32_t big = 0;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)  // NaN is negative here, and left out
+            if (tok + 8 * i + g < len) big = __vmaxs2(big, ds[i][w]);
+          big = __vmaxs2(big, __shfl_xor_sync(kAll, big, 4));
+          big = __vmaxs2(big, __shfl_xor_sync(kAll, big, 8));
+          big = __vmaxs2(big, __shfl_xor_sync(kAll, big, 16));
+          shift[w] = 0;
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const int ex = min(max((int)((big >> (16 * k + 7)) & 255u) - 127, -40), 60);
+            unit[2 * w + k] = ldexpf(1.f, 5 - ex);
+            shift[w] += (uint32_t)((5 - ex) * 128) << (16 * k);
+          }
+        }
+      }
+      if (sizeof(T) == 4) {
+        values_wide<Dv, NB, 3>(acc, tile + S::kV, tile + S::kVStep, tk, unit, hide, lane);
+      } else {
+        // float16 weights hold p step in 11 bits while the step lies in [2, 2^9) of the unit
+        // (exponents 128..135): p is at most 2^6, and from 2^-15 on nothing is lost.  A tile
+        // with another step (a jump of the values' size, a zero, a NaN) goes the wide way.
+        uint32_t off_range = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int w = 0; w < NG / 2; ++w) {
+            ds[i][w] += shift[w];
+            off_range |= ds[i][w] ^ 0x40004000u;
+          }
+        if (__any_sync(kAll, off_range & 0xfc00fc00u))
+          values_wide<Dv, NB, 2>(acc, tile + S::kV, tile + S::kVStep, tk, unit, hide, lane);
+        else
+          values_f16<Dv, NB>(acc, tile + S::kV, ds, tk, lane);
+      }
+    }
+    cp_wait<0>();
+    __syncthreads();  // every slice is done with the ring: the sums go over it
+
+    // ---- the slices' sums, joined
+    float *sum = reinterpret_cast<float *>(smem);
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float y = l[nb][e];
+        y += __shfl_xor_sync(kAll, y, 4);
+        y += __shfl_xor_sync(kAll, y, 8);
+        y += __shfl_xor_sync(kAll, y, 16);
+        const int row = rt * C::kTileRows + 8 * nb + 2 * q + e;
+        if (g == 0) {
+          s_ml[ts][row][0] = mx[nb][e];
+          s_ml[ts][row][1] = y;
+        }
+#pragma unroll
+        for (int j = 0; j < Dv / 16; ++j) {
+          const float back = have_unit ? 1.f / unit[j >> 1] : 0.f;
+          float *to = sum + (ts * C::kRows + row) * C::kSumRow + 16 * j + g;
+          to[0] = acc.o[nb][j][e] * back;
+          to[8] = acc.o[nb][j][2 + e] * back;
+        }
+      }
+    __syncthreads();
+    const bool whole = t0 == 0 && t1 == nt;
+    const int slot = 2 * blockIdx.x + (x - (t1 - t0) == x0 ? 0 : 1);
+    for (int i = tid; i < C::kRows * (Dv / 4); i += kThreads) {
+      const int row = i / (Dv / 4), c = (i - row * (Dv / 4)) * 4;
+      const int gr = rb * C::kRows + row;
+      const int m = gr / a.G, h = hk * a.G + (gr - m * a.G);
+      if (m >= rows) continue;
+      float ref = -CUDART_INF_F;
+#pragma unroll
+      for (int k = 0; k < TS; ++k) ref = fmaxf(ref, s_ml[k][row][0]);
+      const float at = ref == -CUDART_INF_F ? 0.f : ref;
+      float z = 0.f, y[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int k = 0; k < TS; ++k) {
+        const float f = ex2(s_ml[k][row][0] - at);
+        const float4 o = *reinterpret_cast<const float4 *>(sum + (k * C::kRows + row) * C::kSumRow + c);
+        z = fmaf(f, s_ml[k][row][1], z);
+        y[0] = fmaf(f, o.x, y[0]);
+        y[1] = fmaf(f, o.y, y[1]);
+        y[2] = fmaf(f, o.z, y[2]);
+        y[3] = fmaf(f, o.w, y[3]);
+      }
+      if (whole) {
+        const float inv = z == 0.f ? 0.f : 1.f / z;
+        T *dst = (T *)a.O.p + b * a.O.sb + h * a.O.sh + m * a.O.sn + c;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) st_elem(dst + e, y[e] * inv);
+        if (c == 0 && a.lse)
+          a.lse[((int64_t)b * a.H + h) * a.M + m] =
+              z == 0.f ? -CUDART_INF_F : (at + log2f(z)) * 0.693147181f;
+      } else {
+        const int64_t at_row = (int64_t)slot * C::kRows + row;
+        *reinterpret_cast<float4 *>(a.part + at_row * Dv + c) = make_float4(y[0], y[1], y[2], y[3]);
+        if (c == 0)
+          *reinterpret_cast<float2 *>(a.part_ml + at_row * 2) = make_float2(ref, z);
+      }
+    }
+    __syncthreads();  // the ring is free again
+  }
+}
+
+// Rows of items that lie in several stretches (or in none: nothing to see).  One CTA per row:
+// its four warps take the stretches in turn, and their sums are joined in a fixed order.
+template <typename T, int Dv, int kRows>
+__global__ void __launch_bounds__(128) attend_join(const AttendArgs a, const CacheView v, int ctas,
+                                                   int *status) {
+  __shared__ int64_t run[128 + 4];
+  __shared__ float s_m[4], s_l[4], s_o[4][Dv];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int gr = blockIdx.x, hk = blockIdx.y, b = blockIdx.z;
+  const int rows = seq_rows(a, b);
+  if (gr == 0 && hk == 0 && tid == 0) {
+    if (a.counts && rows != a.counts[b]) report(status, MUSE_ERR_DEVICE);
+    if (seq_len(a, v, b) != a.lens[b]) report(status, MUSE_ERR_DEVICE);
+  }
+  const int m = gr / a.G, h = hk * a.G + (gr - m * a.G);
+  const int nt = m < rows ? seq_tiles(a, v, b) : 0;
+  float ref = -CUDART_INF_F, z = 0.f;
+  float y[Dv / 32];
+#pragma unroll
+  for (int e = 0; e < Dv / 32; ++e) y[e] = 0.f;
+  const int rb = gr / kRows, row = gr - rb * kRows;
+  int64_t c0 = 0, c1 = -1, per = 1, start = 0;
+  if (nt) {
+    const int64_t total = line_total<128>(a, v, run);
+    per = stretch(total, ctas, a.min_tiles);
+    // position of sequence b's first tile
+    const int pb = (a.B + 127) / 128, own = b / pb;
+    int64_t first = own ? run[own - 1] : 0;
+    for (int i = own * pb; i < b; ++i) first += (int64_t)seq_tiles(a, v, i) * v.Hkv * a.nrb;
+    start = first + (int64_t)(hk * a.nrb + rb) * nt;
+    c0 = start / per;
+    c1 = (start + nt - 1) / per;
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // on every path: attend ends before this
+  if (m >= rows || c0 == c1) return;                   // finished by its only CTA
+  for (int64_t c = c0 + warp; c <= c1; c += 4) {
+    const int64_t slot = (2 * c + (start <= c * per ? 0 : 1)) * kRows + row;
+    const float2 ml = *reinterpret_cast<const float2 *>(a.part_ml + slot * 2);
+    const float now = fmaxf(ref, ml.x), at = now == -CUDART_INF_F ? 0.f : now;
+    const float fa = ex2(ref - at), fb = ex2(ml.x - at);
+    ref = now;
+    z = z * fa + ml.y * fb;
+#pragma unroll
+    for (int e = 0; e < Dv / 32; ++e) y[e] = y[e] * fa + a.part[slot * Dv + 32 * e + lane] * fb;
   }
   if (lane == 0) {
-    sm[warp] = mx;
-    sl[warp] = l;
+    s_m[warp] = ref;
+    s_l[warp] = z;
   }
 #pragma unroll
-  for (int g = 0; g < NG; ++g) so[warp][32 * g + lane] = o[g];
+  for (int e = 0; e < Dv / 32; ++e) s_o[warp][32 * e + lane] = y[e];
   __syncthreads();
-  float top = fmaxf(fmaxf(sm[0], sm[1]), fmaxf(sm[2], sm[3]));
-  const float ref = top == -CUDART_INF_F ? 0.f : top;
-  float z = 0.f, f[4];
+  float top = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3]));
+  const float at = top == -CUDART_INF_F ? 0.f : top;
+  float zz = 0.f, o = 0.f;
 #pragma unroll
   for (int w = 0; w < 4; ++w) {
-    f[w] = expf(sm[w] - ref);
-    z += f[w] * sl[w];
+    const float f = ex2(s_m[w] - at);
+    zz = fmaf(f, s_l[w], zz);
+    if (tid < Dv) o = fmaf(f, s_o[w][tid], o);
   }
-  const float inv = z == 0.f ? 0.f : 1.f / z;
-  if (tid < Dv) {
-    float y = 0.f;
-#pragma unroll
-    for (int w = 0; w < 4; ++w) y += f[w] * so[w][tid];
-    st_elem((T *)a.O.p + b * a.O.sb + h * a.O.sh + m * a.O.sn + tid, y * inv);
-  }
+  if (tid < Dv)
+    st_elem((T *)a.O.p + b * a.O.sb + h * a.O.sh + m * a.O.sn + tid, zz == 0.f ? 0.f : o / zz);
   if (tid == 0 && a.lse)
-    a.lse[((int64_t)b * a.H + h) * a.M + m] = z == 0.f ? -CUDART_INF_F : ref + logf(z);
+    a.lse[((int64_t)b * a.H + h) * a.M + m] =
+        zz == 0.f ? -CUDART_INF_F : (at + log2f(zz)) * 0.693147181f;
+}
+
+// Rows of a CTA: 8, 16, 32 or blocks of 64 (a warp takes 8 or 16).
+int block_rows(int rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
+
+template <typename T, int D, int Dv, int NB, int RT>
+cudaError_t launch(AttendArgs a, const CacheView &v, int *status, cudaStream_t st) {
+  using C = Shape<T, D, Dv, NB, RT>;
+  const auto kernel = attend<T, D, Dv, NB, RT>;
+  // CTAs that a device holds at once, looked up with the kernel's attribute once a device
+  static std::atomic<int> resident[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  int fit = resident[dev].load(std::memory_order_acquire);
+  if (!fit) {
+    int sms = 0, per_sm = 0;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e == cudaSuccess)
+      e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, 32 * kWarps, C::kSmem);
+    if (e != cudaSuccess) return e;
+    fit = std::max(1, std::min(kMaxCtas, sms * per_sm));
+    resident[dev].store(fit, std::memory_order_release);
+  }
+  const int rows = a.G * a.M;
+  a.nrb = (rows + C::kRows - 1) / C::kRows;
+  a.min_tiles = C::kSlices;
+  // no more CTAs than the table could hold stretches for
+  const int64_t most = (int64_t)a.B * v.Hkv * a.nrb * (((int64_t)v.max_pages << v.page_log2) / kTile);
+  const int ctas = (int)std::min<int64_t>(fit, (most + a.min_tiles - 1) / a.min_tiles);
+  kernel<<<ctas, 32 * kWarps, C::kSmem, st>>>(a, v, status);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(rows, v.Hkv, a.B);
+  cfg.blockDim = dim3(128);
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  count_launches(2);
+  return cudaLaunchKernelEx(&cfg, attend_join<T, Dv, C::kRows>, a, v, ctas, status);
 }
 
 template <typename T, int D, int Dv>
-cudaError_t launch(const AttendArgs &a, const CacheView &v, int *status, cudaStream_t st) {
-  attend_rows<T, D, Dv><<<dim3(a.M, a.H, a.B), 128, 0, st>>>(a, v, status);
-  count_launches(1);
-  return cudaGetLastError();
+cudaError_t by_rows(const AttendArgs &a, const CacheView &v, int *status, cudaStream_t st) {
+  switch (block_rows(a.G * a.M)) {
+    case 8: return launch<T, D, Dv, 1, 1>(a, v, status, st);
+    case 16: return launch<T, D, Dv, 2, 1>(a, v, status, st);
+    case 32: return launch<T, D, Dv, 2, 2>(a, v, status, st);
+    default: return launch<T, D, Dv, 2, 4>(a, v, status, st);
+  }
 }
 
 template <typename T>
 cudaError_t by_width(const AttendArgs &a, const muse_dims &d, const CacheView &v, int *status,
                      cudaStream_t st) {
   if (d.D == 64)
-    return d.Dv == 64 ? launch<T, 64, 64>(a, v, status, st) : launch<T, 64, 128>(a, v, status, st);
-  return d.Dv == 64 ? launch<T, 128, 64>(a, v, status, st) : launch<T, 128, 128>(a, v, status, st);
+    return d.Dv == 64 ? by_rows<T, 64, 64>(a, v, status, st) : by_rows<T, 64, 128>(a, v, status, st);
+  return d.Dv == 64 ? by_rows<T, 128, 64>(a, v, status, st) : by_rows<T, 128, 128>(a, v, status, st);
 }
 
 }  // namespace
 
-size_t cache_attend_ws(const muse_dims &d, int Hkv) { return 256; }
+size_t cache_attend_ws(const muse_dims &d, int Hkv) {
+  const size_t rows = block_rows(d.H / Hkv * d.N);
+  return align_up((size_t)2 * kMaxCtas * rows * d.Dv * 4) + align_up((size_t)2 * kMaxCtas * rows * 8);
+}
 
 cudaError_t run_cache_attend(const muse_rows &Q, const muse_dims &d, const muse_cache &c,
                              const int32_t *lens, const int32_t *counts, const muse_rows &O,
                              float *lse, void *ws, int *status, cudaStream_t st) {
-  const AttendArgs a{Q, O, lse, lens, counts, d.B, d.H, d.N, d.scale};
+  AttendArgs a;
+  a.Q = Q;
+  a.O = O;
+  a.lse = lse;
+  a.lens = lens;
+  a.counts = counts;
+  a.B = d.B;
+  a.H = d.H;
+  a.M = d.N;
+  a.G = d.H / c.Hkv;
+  a.nrb = a.min_tiles = 0;
+  a.scale = d.scale;
+  const size_t rows = block_rows(a.G * a.M);
+  a.part = static_cast<float *>(ws);
+  a.part_ml = reinterpret_cast<float *>(static_cast<char *>(ws) +
+                                        align_up((size_t)2 * kMaxCtas * rows * d.Dv * 4));
   const CacheView v = cache_view(c);
   return d.dtype == MUSE_F32 ? by_width<float>(a, d, v, status, st)
                              : by_width<__nv_bfloat16>(a, d, v, status, st);
