@@ -149,6 +149,13 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// (x & mask) | with in one operation (written out, it becomes two).
+template <uint32_t kMask>
+__device__ __forceinline__ uint32_t picked(uint32_t x, uint32_t with) {
+  uint32_t y;
+  asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(y) : "r"(x), "n"(kMask), "r"(with));
+  return y;
+}
 // Four pairs of codes of a word (nibbles n and n + 4) as float16: 1024 + u, or 1024 + 16 u,
 // without its offset.
 __device__ __forceinline__ void codes_f16(uint32_t x, uint32_t (&c)[4]) {
@@ -156,8 +163,9 @@ __device__ __forceinline__ void codes_f16(uint32_t x, uint32_t (&c)[4]) {
   const __half2 less = __half2half2(__ushort_as_half(0xE408));     // -1032
   const __half2 part = __half2half2(__ushort_as_half(0x2C00));     // 1/16
   const __half2 less16 = __half2half2(__ushort_as_half(0xD480));   // -72
-  uint32_t t[4] = {(x & 0x000f000fu) | 0x64006400u, (x & 0x00f000f0u) | 0x64006400u,
-                   (y & 0x000f000fu) | 0x64006400u, (y & 0x00f000f0u) | 0x64006400u};
+  constexpr uint32_t k1024 = 0x64006400u;
+  uint32_t t[4] = {picked<0x000f000fu>(x, k1024), picked<0x00f000f0u>(x, k1024),
+                   picked<0x000f000fu>(y, k1024), picked<0x00f000f0u>(y, k1024)};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const __half2 h = *reinterpret_cast<const __half2 *>(&t[i]);
@@ -169,7 +177,7 @@ __device__ __forceinline__ void codes_bf16(uint32_t x, uint32_t (&c)[4]) {
   const __nv_bfloat162 less = __bfloat162bfloat162(__ushort_as_bfloat16(0xC308));  // -136
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const uint32_t t = ((x >> (4 * i)) & 0x000f000fu) | 0x43004300u;
+    const uint32_t t = picked<0x000f000fu>(x >> (4 * i), 0x43004300u);
     c[i] = bits(__hadd2(*reinterpret_cast<const __nv_bfloat162 *>(&t), less));
   }
 }
@@ -216,7 +224,7 @@ __device__ __forceinline__ uint32_t value_pair(const uint32_t (&x)[Dv / 32], int
                      grp & 1 ? 0x7632 : 0x5410);
 }
 
-// O^T of 8 NB rows in units of 1 / unit[group]: [rows 8 nb + 2 q + e][channel 16 j + 8 h + g] at
+// O^T of 8 NB rows times unit[group]: row 8 nb + 2 q + e, channel 16 j + 8 h + g at
 // [nb][j][2 h + e].
 template <int Dv, int NB>
 struct Acc {
@@ -235,12 +243,17 @@ struct Hide {
   __device__ __forceinline__ bool at(int nb, int t, int e) const { return edge && t >= left[nb][e]; }
 };
 
-// O += (p vstep) code with float16 weights; ds: the steps as bfloat16 in the accumulators' unit,
-// between 2 and 2^9.
+// O += (p vstep) code with float16 weights; ds: the steps as float16 in the accumulators' unit,
+// in [2^-7, 2), two groups a register.
 template <int Dv, int NB>
 __device__ __forceinline__ void values_f16(Acc<Dv, NB> &acc, const uint8_t *codes,
                                            const uint32_t (&ds)[4][Dv / 64], const Tok<NB> &tk,
                                            int lane) {
+  __half2 p[NB][4];
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) p[nb][i] = __floats2half2_rn(tk.p[nb][i][0], tk.p[nb][i][1]);
 #pragma unroll
   for (int kk = 0; kk < 2; ++kk) {
     uint32_t x[2][Dv / 32];
@@ -248,19 +261,21 @@ __device__ __forceinline__ void values_f16(Acc<Dv, NB> &acc, const uint8_t *code
     words<Dv>(codes, 2 * kk + 1, lane, x[1]);
 #pragma unroll
     for (int grp = 0; grp < Dv / 32; ++grp) {
+      // nibbles n and n + 4 of a pair are channel 8 n + g of the group, of both tokens
       uint32_t c[2][4];
       codes_f16(value_pair<Dv>(x[0], grp), c[0]);
       codes_f16(value_pair<Dv>(x[1], grp), c[1]);
-      // nibbles n and n + 4 of the pair are channel 8 n + g of the group for both tokens: the
-      // half words hold n = 0..3 each
       const uint32_t a0[4] = {c[0][0], c[0][1], c[1][0], c[1][1]};
       const uint32_t a1[4] = {c[0][2], c[0][3], c[1][2], c[1][3]};
-      const float f0 = step_of(ds[2 * kk], grp), f1 = step_of(ds[2 * kk + 1], grp);
+      uint32_t f[2];
+#pragma unroll
+      for (int ii = 0; ii < 2; ++ii)
+        f[ii] = __byte_perm(ds[2 * kk + ii][grp >> 1], 0, grp & 1 ? 0x3232 : 0x1010);
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
-        const float(&p)[4][2] = tk.p[nb];
-        const uint32_t b0 = turned(pack_f16(p[2 * kk][0] * f0, p[2 * kk][1] * f0));
-        const uint32_t b1 = turned(pack_f16(p[2 * kk + 1][0] * f1, p[2 * kk + 1][1] * f1));
+        const uint32_t b0 = turned(bits(__hmul2(p[nb][2 * kk], *reinterpret_cast<__half2 *>(&f[0]))));
+        const uint32_t b1 =
+            turned(bits(__hmul2(p[nb][2 * kk + 1], *reinterpret_cast<__half2 *>(&f[1]))));
         mma_f16(acc.o[nb][2 * grp], a0, b0, b1);
         mma_f16(acc.o[nb][2 * grp + 1], a1, b0, b1);
       }
@@ -325,7 +340,8 @@ __device__ __forceinline__ void values_wide(Acc<Dv, NB> &acc, const uint8_t *cod
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) acc.o[nb][2 * grp + (e >> 2)][e & 3] += t[nb][e >> 2][e & 3];
+      for (int e = 0; e < 8; ++e)
+        acc.o[nb][2 * grp + (e >> 2)][e & 3] += t[nb][e >> 2][e & 3];
   }
 }
 
@@ -335,7 +351,7 @@ struct Shape {
   static constexpr int kSlices = kWarps / RT;
   static constexpr int kTileRows = 8 * NB;
   static constexpr int kRows = kTileRows * RT;
-  static constexpr int kStages = 3;                          // tiles under way of a token slice
+  static constexpr int kStages = 4;                          // tiles under way of a token slice
   static constexpr int kRing = kSlices * kStages * TileShape<D, Dv>::kBytes;
   static constexpr int kSumRow = Dv + 4;                     // so that lanes store to other banks
   static constexpr int kSum = kSlices * kRows * kSumRow * 4; // the slices' sums, over the ring
@@ -344,7 +360,7 @@ struct Shape {
 };
 
 template <typename T, int D, int Dv, int NB, int RT>
-__global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 4 ? 2 : NB == 1 ? 4 : 3)
+__global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 4 ? 2 : 3)
 attend(const AttendArgs a, const CacheView v, int *status) {
   using S = TileShape<D, Dv>;
   using C = Shape<T, D, Dv, NB, RT>;
@@ -388,26 +404,33 @@ attend(const AttendArgs a, const CacheView v, int *status) {
 
     // ---- the slice's tiles t0 + ts, + TS, ...: kStages - 1 of them under way
     const int n_it = max(0, (t1 - t0 - ts + TS - 1) / TS);
-    uint32_t there = 0;  // stages that hold a tile (a page outside the cache is left out)
-    const uint8_t *src = n_it ? cache_tile(v, b, hk, t0 + ts, S::kBytes) : nullptr;
-    auto fetch = [&](int it) {
-      if (it < n_it) {
-        const int st = it % kStages;
+    uint32_t there = 0;     // bit 0: the tile to be used next is there (its page is in the cache)
+    int to_fetch = t0 + ts; // tile to be asked for next, into stage `into`
+    uint32_t into = 0;
+    const uint8_t *src = n_it ? cache_tile(v, b, hk, to_fetch, S::kBytes) : nullptr;
+    auto fetch = [&]() {
+      if (to_fetch < t1) {
         if (src) {
-          for (int i = slice_tid; i < S::kBytes / 16; i += 32 * RT)
-            cp16(ring_s + st * S::kBytes + i * 16, src + i * 16);
-          there |= 1u << st;
-        } else {
-          there &= ~(1u << st);
-          if (slice_tid == 0) report(status, MUSE_ERR_DEVICE);
+#pragma unroll
+          for (int i = 0; i < S::kBytes / 16; i += 32 * RT)
+            if (S::kBytes / 16 % (32 * RT) == 0 || i + slice_tid < S::kBytes / 16)
+              cp16(ring_s + into + (i + slice_tid) * 16, src + (i + slice_tid) * 16);
+          there |= 1u << (kStages - 1);
+        } else if (slice_tid == 0) {
+          report(status, MUSE_ERR_DEVICE);
         }
+        into = into == (kStages - 1) * S::kBytes ? 0 : into + S::kBytes;
+        to_fetch += TS;
         // the next tile's place, asked for a step ahead
-        if (it + 1 < n_it) src = cache_tile(v, b, hk, t0 + ts + (it + 1) * TS, S::kBytes);
+        if (to_fetch < t1) src = cache_tile(v, b, hk, to_fetch, S::kBytes);
       }
       cp_commit();
     };
 #pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) fetch(i);
+    for (int i = 0; i < kStages - 1; ++i) {
+      fetch();
+      there >>= 1;
+    }
 
     // ---- queries as float16 pieces, a power of two a row: this lane's operand is row g
     uint32_t qb[QP][NB][D / 16][2];
@@ -502,14 +525,18 @@ attend(const AttendArgs a, const CacheView v, int *status) {
     float unit[NG];
     bool have_unit = false;
 
+    uint32_t used = 0;
+    int tok = (t0 + ts) * kTile - TS * kTile;
     for (int it = 0; it < n_it; ++it) {
+      const uint8_t *tile = ring + used;
+      used = used == (kStages - 1) * S::kBytes ? 0 : used + S::kBytes;
+      tok += TS * kTile;
       cp_wait<kStages - 2>();
       slice_sync<RT>(ts);
-      const bool here = (there >> (it % kStages)) & 1u;
-      fetch(it + kStages - 1);
+      fetch();
+      const bool here = there & 1u;
+      there >>= 1;
       if (!here) continue;
-      const uint8_t *tile = ring + (it % kStages) * S::kBytes;
-      const int tok = (t0 + ts + it * TS) * kTile;
 
       // ---- logits
       Tok<NB> tk;
@@ -567,7 +594,7 @@ attend(const AttendArgs a, const CacheView v, int *status) {
             for (int e = 0; e < 2; ++e)
               if (hide.at(nb, 8 * i + g, e)) tk.p[nb][i][e] = -CUDART_INF_F;
       }
-      // ---- softmax: the running maximum is a reference, and moves when a weight would pass 2^6
+      // ---- softmax: weights are 2^9 at the reference, which moves when one would pass 2^14
       float top[NB][2];
       bool move = false;
 #pragma unroll
@@ -580,14 +607,14 @@ attend(const AttendArgs a, const CacheView v, int *status) {
           y = fmaxf(y, __shfl_xor_sync(kAll, y, 8));
           y = fmaxf(y, __shfl_xor_sync(kAll, y, 16));
           top[nb][e] = y * rf[nb][e];
-          move |= top[nb][e] > mx[nb][e] + 6.f;
+          move |= top[nb][e] > mx[nb][e] + 14.f;
         }
       if (__any_sync(kAll, move)) {
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const float now = fmaxf(mx[nb][e], top[nb][e]);
+            const float now = fmaxf(mx[nb][e], top[nb][e] - 9.f);
             const float fix = now == -CUDART_INF_F ? 1.f : ex2(mx[nb][e] - now);
             mx[nb][e] = now;
             l[nb][e] *= fix;
@@ -603,15 +630,25 @@ attend(const AttendArgs a, const CacheView v, int *status) {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float &y = tk.p[nb][i][e];
-            y = ex2(fmaf(y, rf[nb][e], -mx[nb][e]));
-            if (hide.at(nb, 8 * i + g, e)) y = 0.f;
-            l[nb][e] += y;
-          }
+          for (int e = 0; e < 2; ++e)
+            tk.p[nb][i][e] = ex2(fmaf(tk.p[nb][i][e], rf[nb][e], -mx[nb][e]));
+      if (hide.edge) {
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              if (hide.at(nb, 8 * i + g, e)) tk.p[nb][i][e] = 0.f;
+      }
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          l[nb][e] += (tk.p[nb][0][e] + tk.p[nb][1][e]) + (tk.p[nb][2][e] + tk.p[nb][3][e]);
 
       // ---- value steps in the unit of the accumulators, which the first tile sets: its largest
-      // step comes to [2^5, 2^6)
+      // step comes to [2^-3, 2^-2)
       uint32_t ds[4][NG / 2];
 #pragma unroll
       for (int i = 0; i < 4; ++i) steps<Dv>(tile + S::kVStep, 8 * i + g, ds[i]);
@@ -630,24 +667,27 @@ attend(const AttendArgs a, const CacheView v, int *status) {
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             const int ex = min(max((int)((big >> (16 * k + 7)) & 255u) - 127, -40), 60);
-            unit[2 * w + k] = ldexpf(1.f, 5 - ex);
-            shift[w] += (uint32_t)((5 - ex) * 128) << (16 * k);
+            unit[2 * w + k] = ldexpf(1.f, -3 - ex);
+            // with float16's exponent: 112 less than bfloat16's
+            shift[w] += (uint32_t)((-3 - ex - 112) * 128) << (16 * k);
           }
         }
       }
       if (sizeof(T) == 4) {
         values_wide<Dv, NB, 3>(acc, tile + S::kV, tile + S::kVStep, tk, unit, hide, lane);
       } else {
-        // float16 weights hold p step in 11 bits while the step lies in [2, 2^9) of the unit
-        // (exponents 128..135): p is at most 2^6, and from 2^-15 on nothing is lost.  A tile
-        // with another step (a jump of the values' size, a zero, a NaN) goes the wide way.
+        // A step in [2^-7, 2) of the unit (exponent field 8..15 of a float16; with bfloat16's 7
+        // bits below it, so one shift is left) is exact, p at most 2^14, and their product a
+        // float16 of 11 bits from p = 2^-7 on, 2^-16 of the reference.  A tile with another step
+        // (a jump of the values' size, a zero, a NaN) goes the wide way.
         uint32_t off_range = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
           for (int w = 0; w < NG / 2; ++w) {
             ds[i][w] += shift[w];
-            off_range |= ds[i][w] ^ 0x40004000u;
+            off_range |= ds[i][w] ^ 0x04000400u;
+            ds[i][w] <<= 3;
           }
         if (__any_sync(kAll, off_range & 0xfc00fc00u))
           values_wide<Dv, NB, 2>(acc, tile + S::kV, tile + S::kVStep, tk, unit, hide, lane);

@@ -291,14 +291,14 @@ def attend_close(got, lse, Q, s, lens, counts, scale, dtype):
     roundings (2u each where a matrix instruction cuts instead of rounding) of the partial sums,
     all below X = s sum|q k|, and a query of 22 bits; exp adds 2 steps of its result and the
     rounding of its argument.  So p is off by a factor of (1 + e), e = (42 u) X + 4 u and the
-    normaliser by as much; products p * step enter in 11 bits (bfloat16 rows) or 22 (float32);
-    their sums, over the tiles of a split, lose 2u a step of 16 tokens.
+    normaliser by as much; p and then p * step are rounded to 11 bits (bfloat16 rows) or p * step
+    to 22 (float32); their sums, over the tiles of a split, lose 2u a step of 16 tokens.
 
-    A bfloat16 row's weight is a float16: below 2^-14 it is held to 2^-25, not to 11 bits.  Its
-    unit is such that some step of the group is 2^5 or more, so that is 2^-30 of the group's
-    largest step, for each of T tokens and times a code of at most 7, over a normaliser that is 1
-    or more in the weights' unit (the reference is some token's own logit): T * 7 * 2^-30 of the
-    largest step.  It shows only in channels where the tokens that the row attends are zero."""
+    A bfloat16 row's p and p * step are float16: below 2^-14 they are held to 2^-25, not to 11
+    bits.  In their unit some step of the group is 2^-3 or more, and the normaliser 2^9 or more
+    (the reference is some token's own logit, and weights there are 2^9): 2^-25 (1 + 2^3) 2^-9
+    < 2^-30 of the group's largest step for each of T tokens, times a code of at most 7.  It shows
+    only in channels where the tokens that the row attends are small or zero."""
     K, V = s.values()
     ref, ref_lse, A, X = so.cache_attend(host(Q), K, V, lens, counts, scale)
     least = np.zeros((Q.shape[0], Q.shape[1], 1, V.shape[-1]))
@@ -309,7 +309,7 @@ def attend_close(got, lse, Q, s, lens, counts, scale, dtype):
             least[b, :, 0] = np.repeat(np.repeat(big, 32, -1), Q.shape[1] // V.shape[1], 0)
     T = max(lens)
     e = (42 * U * X + 4 * U)[..., None]
-    p = 2.0 ** -11 if dtype == BF16 else 2.0 ** -21
+    p = 2.0 ** -10 if dtype == BF16 else 2.0 ** -21
     tol = HALF[dtype] * np.abs(ref) + A * (2 * e + p + 2 * U * (T / 16 + 40)) + least
     for b in range(Q.shape[0]):
         c = counts[b]
