@@ -1,10 +1,13 @@
 // Writing keys and values into the 4-bit cache and reading them back.
 //
 // A group of 32 neighbouring channels of one token has step = bf16(max|x| / 7) and codes
-// round_half_even(x / step).  The code is that of the exact quotient, whatever the type: t =
-// rint(x * (1 / step)) is within one of it, r = x - t step is exact in float32 (t step has at
-// most 12 bits, and r is a multiple of the smaller of the two units and below x), and r
-// against half a step, which is exact too, says whether t has to move.
+// round_half_even(x / step), the code of the exact quotient:
+//   float32: t = rint(x * (1 / step)) is within one of it, r = x - t step is exact in float32
+//   (t step has at most 12 bits, and r is a multiple of the smaller of the two units and below
+//   x), and r against half a step, which is exact too, says whether t has to move;
+//   bfloat16: x and step have 8 bits, so a quotient that is not half-way between two codes is at
+//   least 2^-10 from there.  x * (1 / step), off by 2^-20 at most, is rounded to a multiple of
+//   2^-14, which makes half-way quotients exact, and then to a whole number.
 #include "cache.cuh"
 
 namespace muse {
@@ -27,50 +30,111 @@ __device__ __forceinline__ void load_group(const float *p, float (&x)[32]) {
     x[4 * i + 3] = v.w;
   }
 }
-__device__ __forceinline__ void load_group(const __nv_bfloat16 *p, float (&x)[32]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint4 v = reinterpret_cast<const uint4 *>(p)[i];
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      x[8 * i + 2 * j] = __uint_as_float(w[j] << 16);
-      x[8 * i + 2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
-    }
+// The step of a group whose largest magnitude has these bits; false when it holds an infinity or
+// a NaN.
+__device__ __forceinline__ bool group_step(uint32_t top, float &step, uint16_t &sb) {
+  if (top >= 0x7f800000u) {
+    sb = 0xffffu;
+    return false;
   }
+  const __nv_bfloat16 s = __float2bfloat16_rn(__fdiv_rn(__uint_as_float(top), 7.f));
+  sb = __bfloat16_as_ushort(s);
+  step = __bfloat162float(s);
+  return true;
+}
+// Steps below 2^-100: 1 / step may overflow, and the step may be far from max|x| / 7.
+__device__ __noinline__ uint32_t tiny_code(float x, float step) {
+  const double t = step > 0.f ? rint((double)x / (double)step) : 0.0;
+  return (uint32_t)(int)(fmin(fmax(t, -7.0), 7.0) + 8.0);
 }
 
-// Codes + 8 of a group (x is overwritten by them, as whole numbers) and the step's bits.
-__device__ __forceinline__ uint16_t quantise(float (&x)[32], uint32_t (&u)[32]) {
+// Packs the codes + 8 of a group, u(i) of channel i, into words of eight: for keys the channels
+// in order, for values channel 8 n + g as nibble n of half word g.
+struct KeyOrder {
+  static constexpr int kWords = 4, kNibbles = 8;
+  static __device__ __forceinline__ int channel(int w, int n) { return 8 * w + n; }
+};
+struct ValueOrder {
+  static constexpr int kWords = 8, kNibbles = 4;
+  static __device__ __forceinline__ int channel(int w, int n) { return 8 * n + w; }
+};
+
+template <typename Order>
+__device__ __forceinline__ uint16_t quantise(const float *p, uint32_t (&w)[Order::kWords]) {
+  float x[32];
+  load_group(p, x);
   uint32_t top = 0;
 #pragma unroll
   for (int i = 0; i < 32; ++i) top = max(top, __float_as_uint(x[i]) & 0x7fffffffu);
-  if (top >= 0x7f800000u) {  // an infinity or a NaN
+  float step = 0.f;
+  uint16_t sb;
+  const bool fine = group_step(top, step, sb);
+  const bool tiny = !fine || step < 0x1p-100f;
+  const float inv = tiny ? 0.f : __frcp_rn(step), half = 0.5f * step;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) u[i] = 8;
-    return 0xffffu;
-  }
-  const __nv_bfloat16 sb = __float2bfloat16_rn(__fdiv_rn(__uint_as_float(top), 7.f));
-  const float step = __bfloat162float(sb);
-  if (step < 0x1p-100f) {  // 1 / step may overflow, and the step may be far from max|x| / 7
+  for (int k = 0; k < Order::kWords; ++k) {
+    w[k] = 0;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      const double t = step > 0.f ? rint((double)x[i] / (double)step) : 0.0;
-      u[i] = (uint32_t)(int)(fmin(fmax(t, -7.0), 7.0) + 8.0);
-    }
-  } else {
-    const float inv = __frcp_rn(step), half = 0.5f * step;
-#pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      float t = rintf(x[i] * inv);
-      const float r = fmaf(-t, step, x[i]);
+    for (int n = 0; n < Order::kNibbles; ++n) {
+      const float y = x[Order::channel(k, n)];
+      float t = rintf(y * inv);
+      const float r = fmaf(-t, step, y);
       const bool odd = ((int)t & 1) != 0;
       if (r > half || (r == half && odd)) t += 1.f;
       else if (r < -half || (r == -half && odd)) t -= 1.f;
-      u[i] = (uint32_t)((int)t + 8);
+      const uint32_t u = !fine ? 8u : tiny ? tiny_code(y, step) : (uint32_t)((int)t + 8);
+      w[k] |= u << (4 * n);
     }
   }
-  return __bfloat16_as_ushort(sb);
+  return sb;
+}
+
+template <typename Order>
+__device__ __forceinline__ uint16_t quantise(const __nv_bfloat16 *p, uint32_t (&w)[Order::kWords]) {
+  uint32_t x[16], top2 = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint4 v = reinterpret_cast<const uint4 *>(p)[i];
+    x[4 * i] = v.x;
+    x[4 * i + 1] = v.y;
+    x[4 * i + 2] = v.z;
+    x[4 * i + 3] = v.w;
+  }
+#pragma unroll
+  for (int i = 0; i < 16; ++i) top2 = __vmaxu2(top2, x[i] & 0x7fff7fffu);
+  float step = 0.f;
+  uint16_t sb;
+  const bool fine = group_step(max(top2 << 16, top2 & 0xffff0000u), step, sb);
+  if (fine && step >= 0x1p-100f) {
+    const float inv = __frcp_rn(step);
+#pragma unroll
+    for (int k = 0; k < Order::kWords; ++k) {
+      // a rounded number as bits is 0x4B400000 + 8 + code: the sum of them times 16^n, and what
+      // the constants add up to, modulo 2^32
+      uint32_t sum = 0, less = 0;
+#pragma unroll
+      for (int n = 0; n < Order::kNibbles; ++n) {
+        const int c = Order::channel(k, n);
+        const float y = __uint_as_float(c & 1 ? x[c >> 1] & 0xffff0000u : x[c >> 1] << 16);
+        const float at = fmaf(y, inv, 768.f);               // multiples of 2^-14
+        sum += __float_as_uint(at + 12582152.f) << (4 * n); // 2^23 + 2^22 + 8 - 768
+        less += 0x4B400000u << (4 * n);
+      }
+      w[k] = sum - less;
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < Order::kWords; ++k) {
+      w[k] = 0;
+#pragma unroll
+      for (int n = 0; n < Order::kNibbles; ++n) {
+        const int c = Order::channel(k, n);
+        const float y = __uint_as_float(c & 1 ? x[c >> 1] & 0xffff0000u : x[c >> 1] << 16);
+        w[k] |= (fine ? tiny_code(y, step) : 8u) << (4 * n);
+      }
+    }
+  }
+  return sb;
 }
 
 // One CTA per tile that the call touches: a thread quantises one group of one token into the
@@ -101,34 +165,28 @@ __global__ void __launch_bounds__(D + Dv) cache_write(const CacheRows a, const C
     if (t >= lo && t < hi) {
       const muse_rows &r = key ? a.K : a.V;
       const T *p = (const T *)r.p + b * r.sb + h * r.sh + (n0 + t) * r.sn + grp * 32;
-      float x[32];
-      uint32_t u[32];
-      load_group(p, x);
-      const uint16_t sb = quantise(x, u);
       uint16_t *steps = reinterpret_cast<uint16_t *>(img) + (key ? S::kKStep : S::kVStep) / 2;
-      steps[t * per + grp] = sb;
       if (key) {
+        uint32_t w[4];
+        steps[t * per + grp] = quantise<KeyOrder>(p, w);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          uint32_t w = 0;
-#pragma unroll
-          for (int n = 0; n < 8; ++n) w |= u[8 * q + n] << (4 * n);
-          img[key_word<D>(t, q, grp)] = w;
-        }
+        for (int q = 0; q < 4; ++q) img[key_word<D>(t, q, grp)] = w[q];
       } else {
-        // channels 8 n + g of the group are nibbles 4 (grp % 2) + n of word g: a half word
+        uint32_t w[8];
+        steps[t * per + grp] = quantise<ValueOrder>(p, w);
         uint16_t *half = reinterpret_cast<uint16_t *>(img + S::kV / 4);
 #pragma unroll
-        for (int g = 0; g < 8; ++g) {
-          uint32_t w = 0;
-#pragma unroll
-          for (int n = 0; n < 4; ++n) w |= u[8 * n + g] << (4 * n);
-          half[2 * value_word<Dv>(t, g, grp >> 1) + (grp & 1)] = (uint16_t)w;
-        }
+        for (int g = 0; g < 8; ++g)
+          half[2 * value_word<Dv>(t, g, grp >> 1) + (grp & 1)] = (uint16_t)w[g];
       }
     }
   }
   __syncthreads();
+  if (lo == 0 && hi == kTile) {
+    for (int i = tid; i < S::kBytes / 16; i += kThreads)
+      reinterpret_cast<uint4 *>(dst)[i] = reinterpret_cast<const uint4 *>(img)[i];
+    return;
+  }
   uint32_t *out = reinterpret_cast<uint32_t *>(dst);
   for (int i = tid; i < S::kBytes / 4; i += kThreads) {
     int t;

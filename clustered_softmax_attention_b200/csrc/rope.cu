@@ -7,7 +7,11 @@
 // below 2^-24 half turns and the function's own).
 //
 // Memory-bound: every element is read and written once.  The angles of a row are the same for
-// every head, so a thread keeps VEC sines and cosines and walks the heads with 16-byte loads.
+// every head, so a thread keeps its sines and cosines and walks the heads, four at a time, with
+// the widest loads that both halves of its pairs are aligned for (16 bytes when P is a multiple
+// of 8 in bfloat16, of 4 in float32, or for adjacent pairs; down to one element for odd P).
+#include <algorithm>
+
 #include "internal.h"
 
 namespace muse {
@@ -20,64 +24,159 @@ struct RopeArgs {
   int B, H, Hk, N, heads_per_cta;
 };
 
-template <typename T>
-__device__ __forceinline__ void turn(float &x, float &y, float c, float s) {
-  const float u = x * c - y * s, v = x * s + y * c;
-  x = u;
-  y = v;
-}
-
-__device__ __forceinline__ void pair_angle(const RopeTable &t, const int32_t *pos, int N, int i,
-                                           float &s, float &c) {
+__device__ __forceinline__ void angle(const RopeTable &t, const int32_t *pos, int N, int i,
+                                      float &s, float &c) {
   const int64_t p = pos[(int64_t)t.axis[i] * N];
   const uint64_t ph = (uint64_t)p * t.turn[i];
   sincospif((float)(int32_t)(ph >> 32) * 0x1p-31f, &s, &c);
 }
 
-// One thread per pair (or pair of copied channels) and row: any sections.
-template <typename T, int D>
-__global__ void __launch_bounds__(128) rope_pairs(const RopeArgs a,
-                                                  const __grid_constant__ RopeTable t) {
-  const int64_t id = (int64_t)blockIdx.x * 128 + threadIdx.x;
-  const int64_t row = id / (D / 2);
-  const int i = (int)(id - row * (D / 2));
+// VEC elements as one load; streamed, since nothing is read twice.
+template <typename T, int VEC>
+struct Vec {
+  static constexpr int kBytes = VEC * sizeof(T);
+  uint32_t w[kBytes >= 4 ? kBytes / 4 : 1];
+  __device__ __forceinline__ void load(const T *p) {
+    if (kBytes == 16) {
+      const uint4 v = __ldcs(reinterpret_cast<const uint4 *>(p));
+      w[0] = v.x;
+      w[kBytes / 4 > 1 ? 1 : 0] = v.y;
+      w[kBytes / 4 > 2 ? 2 : 0] = v.z;
+      w[kBytes / 4 > 3 ? 3 : 0] = v.w;
+    } else if (kBytes == 8) {
+      const uint2 v = __ldcs(reinterpret_cast<const uint2 *>(p));
+      w[0] = v.x;
+      w[kBytes / 4 > 1 ? 1 : 0] = v.y;
+    } else if (kBytes == 4) {
+      w[0] = __ldcs(reinterpret_cast<const uint32_t *>(p));
+    } else {
+      w[0] = __ldcs(reinterpret_cast<const uint16_t *>(p));
+    }
+  }
+  __device__ __forceinline__ void store(T *p) const {
+    if (kBytes == 16)
+      __stcs(reinterpret_cast<uint4 *>(p), make_uint4(w[0], w[kBytes / 4 > 1 ? 1 : 0],
+                                                      w[kBytes / 4 > 2 ? 2 : 0], w[kBytes / 4 > 3 ? 3 : 0]));
+    else if (kBytes == 8)
+      __stcs(reinterpret_cast<uint2 *>(p), make_uint2(w[0], w[kBytes / 4 > 1 ? 1 : 0]));
+    else if (kBytes == 4) __stcs(reinterpret_cast<uint32_t *>(p), w[0]);
+    else __stcs(reinterpret_cast<uint16_t *>(p), (uint16_t)w[0]);
+  }
+  __device__ __forceinline__ float get(int i) const {
+    if (sizeof(T) == 4) return __uint_as_float(w[i]);
+    return __uint_as_float(i & 1 ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
+  }
+  // elements i and i + 1 (i even), or the only one
+  __device__ __forceinline__ void set(int i, float x, float y) {
+    if (sizeof(T) == 4) {
+      w[i] = __float_as_uint(x);
+      if (VEC > 1) w[VEC > 1 ? i + 1 : i] = __float_as_uint(y);
+    } else {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+      w[i >> 1] = *reinterpret_cast<const uint32_t *>(&h);
+    }
+  }
+};
+
+constexpr int kThreads = 128;
+constexpr int kHeads = 4;  // heads whose loads are under way together
+
+// A thread owns two vectors of a row: the two halves of VEC pairs, two vectors of adjacent
+// pairs, or two vectors that are copied.
+template <typename T, int D, int VEC, bool ADJ>
+__global__ void __launch_bounds__(kThreads) rope(const RopeArgs a, const __grid_constant__ RopeTable t) {
+  constexpr int kRow = D / (2 * VEC);  // threads of a row
+  const int64_t id = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+  const int64_t row = id / kRow;
+  const int u = (int)(id - row * kRow);
   if (row >= (int64_t)a.B * a.N) return;
   const int b = (int)(row / a.N), n = (int)(row - (int64_t)b * a.N);
-  const bool turned = i < t.P;
-  const int c0 = !turned || t.adjacent ? 2 * i : i;
-  const int c1 = !turned || t.adjacent ? 2 * i + 1 : i + t.P;
-  float s = 0.f, c = 1.f;
-  if (turned) pair_angle(t, a.pos + b * a.pos_sb + n, a.N, i, s, c);
+  // channels of the two vectors, and the first pair of each (P or more: copied)
+  int c0, c1;
+  if (ADJ) {
+    c0 = u * VEC;
+    c1 = c0 + D / 2;
+  } else {
+    const int turned = t.P / VEC;
+    c0 = u < turned ? u * VEC : 2 * t.P + (u - turned) * 2 * VEC;
+    c1 = u < turned ? t.P + u * VEC : c0 + VEC;
+  }
+  float sn[VEC], cs[VEC];
+  const int32_t *pos = a.pos + b * a.pos_sb + n;
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) {
+    const int pair = ADJ ? (i < VEC / 2 ? c0 / 2 + i : c1 / 2 + i - VEC / 2) : u * VEC + i;
+    sn[i] = 0.f;
+    cs[i] = 1.f;
+    if (pair < t.P) angle(t, pos, a.N, pair, sn[i], cs[i]);
+  }
   const int h1 = min(a.H + a.Hk, (int)(blockIdx.y + 1) * a.heads_per_cta);
-  for (int h = blockIdx.y * a.heads_per_cta; h < h1; ++h) {
-    const bool q = h < a.H;
-    const muse_rows &in = q ? a.Q : a.K, &out = q ? a.Qo : a.Ko;
-    const int hh = q ? h : h - a.H;
-    const T *x = (const T *)in.p + b * in.sb + hh * in.sh + n * in.sn;
-    T *y = (T *)out.p + b * out.sb + hh * out.sh + n * out.sn;
-    const T e0 = x[c0], e1 = x[c1];
-    if (turned) {
-      float u = ld_elem(&e0), v = ld_elem(&e1);
-      turn<T>(u, v, c, s);
-      st_elem(y + c0, u);
-      st_elem(y + c1, v);
-    } else {
-      y[c0] = e0;
-      y[c1] = e1;
+  for (int h0 = blockIdx.y * a.heads_per_cta; h0 < h1; h0 += kHeads) {
+    Vec<T, VEC> x[kHeads], y[kHeads];
+#pragma unroll
+    for (int k = 0; k < kHeads; ++k) {
+      const int h = h0 + k;
+      if (h >= h1) break;
+      const muse_rows &r = h < a.H ? a.Q : a.K;
+      const T *p = (const T *)r.p + b * r.sb + (h < a.H ? h : h - a.H) * r.sh + n * r.sn;
+      x[k].load(p + c0);
+      y[k].load(p + c1);
+    }
+#pragma unroll
+    for (int k = 0; k < kHeads; ++k) {
+      const int h = h0 + k;
+      if (h >= h1) break;
+      const muse_rows &r = h < a.H ? a.Qo : a.Ko;
+      T *p = (T *)r.p + b * r.sb + (h < a.H ? h : h - a.H) * r.sh + n * r.sn;
+      if (ADJ) {
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+          Vec<T, VEC> &z = v ? y[k] : x[k];
+#pragma unroll
+          for (int i = 0; i < VEC / 2; ++i) {
+            const float s = sn[v * VEC / 2 + i], c = cs[v * VEC / 2 + i];
+            const float e = z.get(2 * i), f = z.get(2 * i + 1);
+            // a copied pair stays as it is, whatever it holds
+            if ((v ? c1 : c0) / 2 + i < t.P) z.set(2 * i, e * c - f * s, e * s + f * c);
+          }
+        }
+      } else if (u * VEC < t.P) {
+#pragma unroll
+        for (int i = 0; i < VEC; i += 2) {
+          const int j = VEC > 1 ? i + 1 : i;
+          const float e0 = x[k].get(i), f0 = y[k].get(i), e1 = x[k].get(j), f1 = y[k].get(j);
+          x[k].set(i, e0 * cs[i] - f0 * sn[i], e1 * cs[j] - f1 * sn[j]);
+          y[k].set(i, e0 * sn[i] + f0 * cs[i], e1 * sn[j] + f1 * cs[j]);
+        }
+      }
+      x[k].store(p + c0);
+      y[k].store(p + c1);
     }
   }
 }
 
-template <typename T, int D>
-cudaError_t launch(const RopeArgs &a0, const RopeTable &t, cudaStream_t st) {
-  RopeArgs a = a0;
-  const int64_t work = (int64_t)a.B * a.N * (D / 2);
-  const int64_t ctas = (work + 127) / 128;
+template <typename T, int D, int VEC, bool ADJ>
+cudaError_t launch(RopeArgs a, const RopeTable &t, cudaStream_t st) {
+  const int heads = a.H + a.Hk;
+  const int64_t ctas = ((int64_t)a.B * a.N * (D / (2 * VEC)) + kThreads - 1) / kThreads;
   if (ctas > 0x7fffffff) return cudaErrorInvalidValue;
-  a.heads_per_cta = a.H + a.Hk;
-  rope_pairs<T, D><<<dim3((unsigned)ctas, 1), 128, 0, st>>>(a, t);
+  // all heads to a thread once that fills the card (angles are worth about four heads' work)
+  const int64_t split = std::max<int64_t>(1, std::min<int64_t>(heads, (148 * 8 + ctas - 1) / ctas));
+  a.heads_per_cta = (int)((heads + split - 1) / split);
+  const unsigned groups = (unsigned)((heads + a.heads_per_cta - 1) / a.heads_per_cta);
+  rope<T, D, VEC, ADJ><<<dim3((unsigned)ctas, groups), kThreads, 0, st>>>(a, t);
   count_launches(1);
   return cudaGetLastError();
+}
+
+template <typename T, int D>
+cudaError_t by_width(const RopeArgs &a, const RopeTable &t, cudaStream_t st) {
+  constexpr int kWide = 16 / sizeof(T);
+  if (t.adjacent) return launch<T, D, kWide, true>(a, t, st);
+  if (t.P % kWide == 0) return launch<T, D, kWide, false>(a, t, st);
+  if (t.P % (kWide / 2) == 0) return launch<T, D, kWide / 2, false>(a, t, st);
+  if (t.P % 2 == 0) return launch<T, D, 2, false>(a, t, st);
+  return launch<T, D, 1, false>(a, t, st);
 }
 
 }  // namespace
@@ -96,8 +195,9 @@ cudaError_t run_rope(const muse_rows &Q, const muse_rows &K, int Hk, const muse_
   a.H = d.H;
   a.Hk = Hk;
   a.N = d.N;
-  if (d.dtype == MUSE_F32) return d.D == 64 ? launch<float, 64>(a, t, st) : launch<float, 128>(a, t, st);
-  return d.D == 64 ? launch<__nv_bfloat16, 64>(a, t, st) : launch<__nv_bfloat16, 128>(a, t, st);
+  if (d.dtype == MUSE_F32)
+    return d.D == 64 ? by_width<float, 64>(a, t, st) : by_width<float, 128>(a, t, st);
+  return d.D == 64 ? by_width<__nv_bfloat16, 64>(a, t, st) : by_width<__nv_bfloat16, 128>(a, t, st);
 }
 
 }  // namespace muse

@@ -59,14 +59,14 @@ static bool rope_table(const muse_rope &r, int D, RopeTable &t) {
   t.axes = r.axes;
   t.adjacent = (r.flags & MUSE_ROPE_ADJACENT) != 0;
   const long double two_pi = 6.283185307179586476925286766559005768L;
-  for (int a = 0, i = 0, first = 0; a < r.axes; first += r.sections[a], ++a) {
-    for (int j = 0; j < r.sections[a]; ++j, ++i) {
-      const long double e = (r.flags & MUSE_ROPE_AXIS_LADDER)
-                                ? (long double)(i - first) / r.sections[a]
-                                : (long double)i / P;
+  for (int a = 0, i = 0; a < r.axes; ++a) {
+    // base^-e down a ladder by its ratio: 64 products of 64 bits lose no more than 2^-58
+    const bool own = (r.flags & MUSE_ROPE_AXIS_LADDER) != 0;
+    const long double ratio = powl((long double)r.base, -1.0L / (own ? r.sections[a] : P));
+    long double f = own ? 1.0L : powl(ratio, i);
+    for (int j = 0; j < r.sections[a]; ++j, ++i, f *= ratio) {
       // below 1 / (2 pi) of a turn, so the fraction fits
-      const long double f = powl((long double)r.base, -e) / two_pi;
-      uint64_t u = (uint64_t)ldexpl(f, 64);
+      const uint64_t u = (uint64_t)(f / two_pi * 18446744073709551616.0L);
       t.turn[i] = (r.flags & MUSE_ROPE_INVERSE) ? 0 - u : u;
       t.axis[i] = (uint8_t)a;
     }
