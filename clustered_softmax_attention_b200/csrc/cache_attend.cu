@@ -13,7 +13,9 @@
 // Work is split evenly whatever the lengths: the 32-token tiles of all (sequence, head, row
 // block) items form one line, and every CTA takes a stretch of it.  An item that lies in one
 // stretch is finished there; the others leave float32 partial sums (at most two a CTA), which
-// attend_join adds in the order of the CTAs: results do not depend on timing.
+// attend_join adds in the order of the CTAs: results do not depend on timing.  Where no sequence
+// can be long, a cluster of CTAs takes an item instead and joins its sums through distributed
+// shared memory: one launch.
 #include <algorithm>
 #include <atomic>
 
@@ -26,6 +28,8 @@ namespace {
 
 constexpr int kMaxCtas = 592;   // 148 SMs x 4: the bound of the partials in the workspace
 constexpr int kWarps = 4;
+constexpr int kCluster = 8;      // CTAs of a cluster that takes an item
+constexpr int kClusterTiles = 16;  // of a token slice: the longest table that clusters take
 struct AttendArgs {
   muse_rows Q, O;
   float *lse;
@@ -33,9 +37,11 @@ struct AttendArgs {
   int B, H, M, G;      // G = H / Hkv
   int nrb;             // row blocks of an item's G * M rows
   int min_tiles;       // a CTA takes at least so many
+  int cluster;         // CTAs of an item, or 0: stretches of the line
   float scale;
   float *part;         // [2 kMaxCtas][rows of a block][Dv]
   float *part_ml;      // [2 kMaxCtas][rows of a block][2]
+  int2 *ends;          // [items]: slot of an item's first part, CTA of its last
 };
 
 // New rows, and tokens that the last of them may see, of sequence b.
@@ -47,8 +53,24 @@ __device__ __forceinline__ int seq_len(const AttendArgs &a, const CacheView &v, 
   const int64_t cap = (int64_t)v.max_pages << v.page_log2;
   return (int)min((int64_t)max(a.lens[b], 0), cap);
 }
+// Lengths and counts outside their range: those tokens and rows are left out.
+__device__ __forceinline__ void check_lengths(const AttendArgs &a, const CacheView &v, int b,
+                                              int *status) {
+  if ((a.counts && seq_rows(a, b) != a.counts[b]) || seq_len(a, v, b) != a.lens[b])
+    report(status, MUSE_ERR_DEVICE);
+}
 __device__ __forceinline__ int seq_tiles(const AttendArgs &a, const CacheView &v, int b) {
   return seq_rows(a, b) ? (seq_len(a, v, b) + kTile - 1) / kTile : 0;
+}
+
+// Beginning and ending an item (its queries, joining its sums) takes a CTA as long as kItemTiles
+// tiles: so many places on the line come before each item's tiles.  48 sequences of 0 to 8192
+// tokens, 8 heads: 182 us with 0, 93 with 6 and 10, 81 with 16; as many tokens in sequences of
+// one length: 79.
+constexpr int kItemTiles = 16;
+__device__ __forceinline__ int64_t seq_units(const AttendArgs &a, const CacheView &v, int b) {
+  const int nt = seq_tiles(a, v, b);
+  return nt ? (int64_t)(nt + kItemTiles) * v.Hkv * a.nrb : 0;
 }
 
 // The line of tiles: its length, and the sequence in which position x lies with the position
@@ -62,7 +84,7 @@ __device__ __forceinline__ int64_t line_total(const AttendArgs &a, const CacheVi
   const int tid = threadIdx.x, per = (a.B + kThreads - 1) / kThreads;
   const int b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
   int64_t s = 0;
-  for (int b = b0; b < b1; ++b) s += seq_tiles(a, v, b);
+  for (int b = b0; b < b1; ++b) s += seq_units(a, v, b);
   // inclusive scan over the threads
   const int lane = tid & 31, warp = tid >> 5;
 #pragma unroll
@@ -74,7 +96,7 @@ __device__ __forceinline__ int64_t line_total(const AttendArgs &a, const CacheVi
   __syncthreads();
   int64_t add = 0;
   for (int w = 0; w < warp; ++w) add += run[kThreads + w];
-  run[tid] = (s + add) * v.Hkv * a.nrb;
+  run[tid] = s + add;
   __syncthreads();
   return run[kThreads - 1];
 }
@@ -91,14 +113,48 @@ __device__ __forceinline__ void line_find(const AttendArgs &a, const CacheView &
   b = lo * per;
   first = lo ? run[lo - 1] : 0;
   while (b < a.B - 1) {
-    const int64_t n = (int64_t)seq_tiles(a, v, b) * v.Hkv * a.nrb;
+    const int64_t n = seq_units(a, v, b);
     if (first + n > x) break;
     first += n;
     ++b;
   }
 }
-__device__ __forceinline__ int64_t stretch(int64_t total, int ctas, int min_tiles) {
-  return max((int64_t)min_tiles, (total + ctas - 1) / ctas);
+// A CTA's walk along the line, from x to x1, and the part of one item that it has come to.
+struct Walk {
+  int64_t x, x1, first;  // first: position of sequence b's first item
+  int b;
+};
+struct Span {
+  int b, hk, rb, t0, t1, nt, len, rows;
+  int parts_in;  // CTAs, from this one on, that the item's tiles lie in (where t0 is 0)
+};
+__device__ __noinline__ bool next_span(const AttendArgs &a, const CacheView &v, Walk &w, Span &s,
+                                       int64_t per) {
+  while (w.x < w.x1) {
+    int64_t units = seq_units(a, v, w.b);
+    while (w.x >= w.first + units) {
+      w.first += units;
+      units = seq_units(a, v, ++w.b);
+    }
+    const int nt = seq_tiles(a, v, w.b);
+    const int64_t in = w.x - w.first;
+    const uint32_t one = (uint32_t)(nt + kItemTiles);
+    const int item = in >> 32 ? (int)(in / one) : (int)((uint32_t)in / one);
+    const int64_t start = w.first + (int64_t)item * one + kItemTiles;  // of its tiles
+    s.b = w.b;
+    s.hk = item / a.nrb;
+    s.rb = item - s.hk * a.nrb;
+    s.nt = nt;
+    s.t0 = (int)max((int64_t)0, w.x - start);
+    s.t1 = (int)max((int64_t)0, min((int64_t)nt, w.x1 - start));
+    s.len = seq_len(a, v, w.b);
+    s.rows = seq_rows(a, w.b);
+    const int64_t left = w.x1 - start;  // tiles of the item up to this stretch's end
+    s.parts_in = left >= nt ? 1 : 1 + (int)((nt - left + per - 1) / per);
+    w.x = left >= nt ? start + nt : w.x1;
+    if (s.t0 < s.t1) return true;
+  }
+  return false;
 }
 
 // ------------------------------------------------------------------ small device pieces
@@ -110,6 +166,22 @@ __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_grou
 template <int N>
 __device__ __forceinline__ void cp_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ float4 cluster_ld4(const float *p, int rank) {
+  uint32_t at;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;"
+      : "=r"(at)
+      : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
+  float4 x;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
+               : "r"(at)
+               : "memory");
+  return x;
 }
 template <int N>
 __device__ __forceinline__ void slice_sync(int slice) {  // the N warps of a token slice
@@ -267,15 +339,16 @@ __device__ __forceinline__ void values_f16(Acc<Dv, NB> &acc, const uint8_t *code
       codes_f16(value_pair<Dv>(x[1], grp), c[1]);
       const uint32_t a0[4] = {c[0][0], c[0][1], c[1][0], c[1][1]};
       const uint32_t a1[4] = {c[0][2], c[0][3], c[1][2], c[1][3]};
-      uint32_t f[2];
+      __half2 f[2];
 #pragma unroll
-      for (int ii = 0; ii < 2; ++ii)
-        f[ii] = __byte_perm(ds[2 * kk + ii][grp >> 1], 0, grp & 1 ? 0x3232 : 0x1010);
+      for (int ii = 0; ii < 2; ++ii) {
+        const __half2 x2 = *reinterpret_cast<const __half2 *>(&ds[2 * kk + ii][grp >> 1]);
+        f[ii] = grp & 1 ? __high2half2(x2) : __low2half2(x2);
+      }
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
-        const uint32_t b0 = turned(bits(__hmul2(p[nb][2 * kk], *reinterpret_cast<__half2 *>(&f[0]))));
-        const uint32_t b1 =
-            turned(bits(__hmul2(p[nb][2 * kk + 1], *reinterpret_cast<__half2 *>(&f[1]))));
+        const uint32_t b0 = turned(bits(__hmul2(p[nb][2 * kk], f[0])));
+        const uint32_t b1 = turned(bits(__hmul2(p[nb][2 * kk + 1], f[1])));
         mma_f16(acc.o[nb][2 * grp], a0, b0, b1);
         mma_f16(acc.o[nb][2 * grp + 1], a1, b0, b1);
       }
@@ -345,23 +418,42 @@ __device__ __forceinline__ void values_wide(Acc<Dv, NB> &acc, const uint8_t *cod
   }
 }
 
+// Four channels of a row: sums y over weights of sum z at reference `at`.
+template <typename T>
+__device__ __forceinline__ void finish_row(const AttendArgs &a, int b, int h, int m, int c,
+                                           const float (&y)[4], float z, float at) {
+  const float inv = z == 0.f ? 0.f : 1.f / z;  // a row that sees nothing is zero
+  T *dst = (T *)a.O.p + b * a.O.sb + h * a.O.sh + m * a.O.sn + c;
+  if (sizeof(T) == 4) {
+    *reinterpret_cast<float4 *>(dst) = make_float4(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv);
+  } else {
+    *reinterpret_cast<uint2 *>(dst) = make_uint2(bits(__floats2bfloat162_rn(y[0] * inv, y[1] * inv)),
+                                                 bits(__floats2bfloat162_rn(y[2] * inv, y[3] * inv)));
+  }
+  if (c == 0 && a.lse)
+    a.lse[((int64_t)b * a.H + h) * a.M + m] =
+        z == 0.f ? -CUDART_INF_F : (at + log2f(z)) * 0.693147181f;
+}
+
 // One CTA: RT row tiles of 8 NB x kWarps / RT token slices.
 template <typename T, int D, int Dv, int NB, int RT>
 struct Shape {
   static constexpr int kSlices = kWarps / RT;
   static constexpr int kTileRows = 8 * NB;
   static constexpr int kRows = kTileRows * RT;
-  static constexpr int kStages = 4;                          // tiles under way of a token slice
+  static constexpr int kStages = RT == 1 ? 3 : 4;            // tiles under way of a token slice
   static constexpr int kRing = kSlices * kStages * TileShape<D, Dv>::kBytes;
   static constexpr int kSumRow = Dv + 4;                     // so that lanes store to other banks
-  static constexpr int kSum = kSlices * kRows * kSumRow * 4; // the slices' sums, over the ring
-  static constexpr int kSmem = kRing > kSum ? kRing : kSum;
+  static constexpr int kSum = kWarps * 8 * kSumRow * 4;      // eight rows of every warp
+  static constexpr int kSmem = kRing + kSum;
+  static constexpr bool kClusters = kRows * kSumRow * 4 <= kRing;  // an item's rows, over the ring
+  static constexpr int kLoads = sizeof(T) / 2;               // 16-byte loads of eight channels
   static constexpr int kParts = sizeof(T) == 4 ? 2 : 1;      // float16 pieces of a query
 };
 
 template <typename T, int D, int Dv, int NB, int RT>
-__global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 4 ? 2 : 3)
-attend(const AttendArgs a, const CacheView v, int *status) {
+__global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 4 || (NB == 2 && Dv == 128) ? 2 : 3)
+attend(const __grid_constant__ AttendArgs a, const __grid_constant__ CacheView v, int *status) {
   using S = TileShape<D, Dv>;
   using C = Shape<T, D, Dv, NB, RT>;
   constexpr int NGk = D / 32, NG = Dv / 32, TS = C::kSlices, kThreads = 32 * kWarps;
@@ -369,137 +461,167 @@ attend(const AttendArgs a, const CacheView v, int *status) {
   constexpr unsigned kAll = 0xffffffffu;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int64_t run[kThreads + kWarps];
-  __shared__ float s_ml[TS][C::kRows][2];
+  __shared__ float s_ml[TS][RT * 8][2];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q = lane & 3;
   const int rt = warp % RT, ts = warp / RT;
 
-  const int64_t total = line_total<kThreads>(a, v, run);
-  const int64_t per = stretch(total, gridDim.x, a.min_tiles);
-  const int64_t x0 = blockIdx.x * per, x1 = min(total, x0 + per);
+  // ---- what this CTA does: a stretch of the line, or its part of its cluster's item
+  Walk walk;
+  Span sp;
+  int64_t per = 1;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (x0 >= x1) return;
-  int b;
-  int64_t first;
-  line_find<kThreads>(a, v, run, x0, b, first);
+  if (C::kClusters && a.cluster) {
+    const int rank = blockIdx.x % a.cluster, item = blockIdx.x / a.cluster;
+    sp.b = item / (v.Hkv * a.nrb);
+    sp.hk = item / a.nrb % v.Hkv;
+    sp.rb = item % a.nrb;
+    sp.nt = seq_tiles(a, v, sp.b);
+    sp.t0 = sp.nt * rank / a.cluster;
+    sp.t1 = sp.nt * (rank + 1) / a.cluster;
+    sp.len = seq_len(a, v, sp.b);
+    sp.rows = seq_rows(a, sp.b);
+    walk.x = walk.x1 = 0;
+    if (rank == 0 && sp.hk == 0 && sp.rb == 0 && tid == 0) check_lengths(a, v, sp.b, status);
+  } else {
+    const int64_t total = line_total<kThreads>(a, v, run);
+    per = max((int64_t)a.min_tiles, (total + gridDim.x - 1) / gridDim.x);
+    walk.x = blockIdx.x * per;
+    walk.x1 = min(total, walk.x + per);
+    if (walk.x >= walk.x1) return;
+    line_find<kThreads>(a, v, run, walk.x, walk.b, walk.first);
+    if (!next_span(a, v, walk, sp, per)) return;
+  }
 
   uint8_t *ring = smem + ts * kStages * S::kBytes;
+  float *sum = reinterpret_cast<float *>(smem + C::kRing);
   const uint32_t ring_s = (uint32_t)__cvta_generic_to_shared(ring);
   const int slice_tid = rt * 32 + lane;
 
-  int64_t x = x0;
-  int nt = seq_tiles(a, v, b), len = seq_len(a, v, b), rows = seq_rows(a, b);
-  while (x < x1) {
-    // the item of position x, and the part [t0, t1) of its nt tiles in this stretch
-    while (x >= first + (int64_t)nt * v.Hkv * a.nrb) {
-      first += (int64_t)nt * v.Hkv * a.nrb;
-      ++b;
-      nt = seq_tiles(a, v, b);
-      len = seq_len(a, v, b);
-      rows = seq_rows(a, b);
+  // ---- the slice's tiles t0 + ts, + TS, ... of one span after the other: kStages - 1 of them are
+  // under way, across spans too
+  Walk ahead = walk;
+  int f_tile = sp.t0 + ts, f_end = sp.t1;
+  uint32_t there = 0;  // bit 0: the tile to be used next is there (its page is in the cache)
+  uint32_t into = 0, used = 0;
+  const uint8_t *src = nullptr;
+  // a head's tiles of page 0, the sequence's pages, and from page to page in units of 128 bytes
+  const int per_log2 = v.page_log2 - 5, per_mask = (1 << per_log2) - 1;
+  const uint32_t page_units = ((uint32_t)v.Hkv * (S::kBytes / 128)) << per_log2;
+  const uint8_t *f_head;
+  const int32_t *f_pages;
+  auto begin = [&](const Span &to) {
+    f_head = v.tiles + (((int64_t)to.hk * S::kBytes) << per_log2);
+    f_pages = v.table + (int64_t)to.b * v.max_pages;
+    f_tile = to.t0 + ts;
+    f_end = to.t1;
+  };
+  begin(sp);
+  auto place = [&]() {  // where the next tile lies, asked for a step before it is fetched
+    while (f_tile >= f_end) {
+      Span n;
+      if (!next_span(a, v, ahead, n, per)) return;
+      begin(n);
     }
-    const int item = (int)((x - first) / nt), hk = item / a.nrb, rb = item - hk * a.nrb;
-    const int t0 = (int)((x - first) - (int64_t)item * nt);
-    const int t1 = (int)min((int64_t)nt, t0 + (x1 - x));
-    x += t1 - t0;
-
-    // ---- the slice's tiles t0 + ts, + TS, ...: kStages - 1 of them under way
-    const int n_it = max(0, (t1 - t0 - ts + TS - 1) / TS);
-    uint32_t there = 0;     // bit 0: the tile to be used next is there (its page is in the cache)
-    int to_fetch = t0 + ts; // tile to be asked for next, into stage `into`
-    uint32_t into = 0;
-    const uint8_t *src = n_it ? cache_tile(v, b, hk, to_fetch, S::kBytes) : nullptr;
-    auto fetch = [&]() {
-      if (to_fetch < t1) {
-        if (src) {
+    const uint32_t pg = (uint32_t)f_pages[f_tile >> per_log2];
+    src = pg < (uint32_t)v.pages
+              ? f_head + ((uint64_t)pg * page_units << 7) + (uint32_t)((f_tile & per_mask) * S::kBytes)
+              : nullptr;
+  };
+  auto fetch = [&]() {
+    if (f_tile < f_end) {
+      if (src) {
 #pragma unroll
-          for (int i = 0; i < S::kBytes / 16; i += 32 * RT)
-            if (S::kBytes / 16 % (32 * RT) == 0 || i + slice_tid < S::kBytes / 16)
-              cp16(ring_s + into + (i + slice_tid) * 16, src + (i + slice_tid) * 16);
-          there |= 1u << (kStages - 1);
-        } else if (slice_tid == 0) {
-          report(status, MUSE_ERR_DEVICE);
-        }
-        into = into == (kStages - 1) * S::kBytes ? 0 : into + S::kBytes;
-        to_fetch += TS;
-        // the next tile's place, asked for a step ahead
-        if (to_fetch < t1) src = cache_tile(v, b, hk, to_fetch, S::kBytes);
+        for (int i = 0; i < S::kBytes / 16; i += 32 * RT)
+          if (S::kBytes / 16 % (32 * RT) == 0 || i + slice_tid < S::kBytes / 16)
+            cp16(ring_s + into + (i + slice_tid) * 16, src + (i + slice_tid) * 16);
+        there |= 1u << (kStages - 1);
+      } else if (slice_tid == 0) {
+        report(status, MUSE_ERR_DEVICE);
       }
-      cp_commit();
-    };
-#pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) {
-      fetch();
-      there >>= 1;
+      into = into == (kStages - 1) * S::kBytes ? 0 : into + S::kBytes;
+      f_tile += TS;
+      place();
     }
+    cp_commit();
+  };
+  place();
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) {
+    fetch();
+    there >>= 1;
+  }
 
-    // ---- queries as float16 pieces, a power of two a row: this lane's operand is row g
+  // this lane's part of row 8 nb + g: channels 32 w + 8 q + (0..7)
+  uint4 raw[NB][NGk * C::kLoads];
+  auto load_rows = [&](const Span &to) {
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+      const int row = to.rb * C::kRows + rt * C::kTileRows + 8 * nb + g;
+      const int m = row / a.G, h = to.hk * a.G + (row - m * a.G);
+      const T *from = (const T *)a.Q.p + to.b * a.Q.sb + h * a.Q.sh + m * a.Q.sn + 8 * q;
+#pragma unroll
+      for (int i = 0; i < NGk * C::kLoads; ++i)
+        raw[nb][i] = m < to.rows ? reinterpret_cast<const uint4 *>(
+                                       from + 32 * (i / C::kLoads))[i % C::kLoads]
+                                 : make_uint4(0, 0, 0, 0);
+    }
+  };
+  load_rows(sp);
+
+  for (int spans = 0;; ++spans) {
+    const int n_it = max(0, (sp.t1 - sp.t0 - ts + TS - 1) / TS);
+
+    // ---- queries as float16 pieces, a power of two a row
     uint32_t qb[QP][NB][D / 16][2];
     float rf[NB][2];     // rows 2 q + e from here on
     int see[NB][2], see_all = 0x7fffffff;
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
-      const int row0 = rb * C::kRows + rt * C::kTileRows + 8 * nb;
-      const int m = (row0 + g) / a.G, h = hk * a.G + (row0 + g - m * a.G);
-      const T *from = (const T *)a.Q.p + b * a.Q.sb + h * a.Q.sh + m * a.Q.sn;
-      float f[NGk][8], top = 0.f;
-      bool bad = false;
+      uint32_t top = 0;  // the largest magnitude's bits: an infinity or a NaN is above all others
 #pragma unroll
-      for (int w = 0; w < NGk; ++w) {
-        if (m >= rows) {
+      for (int i = 0; i < NGk * C::kLoads; ++i) {
+        const uint32_t x[4] = {raw[nb][i].x, raw[nb][i].y, raw[nb][i].z, raw[nb][i].w};
 #pragma unroll
-          for (int n = 0; n < 8; ++n) f[w][n] = 0.f;
-        } else if (sizeof(T) == 4) {
-          const float4 u0 = *reinterpret_cast<const float4 *>(from + 32 * w + 8 * q);
-          const float4 u1 = *reinterpret_cast<const float4 *>(from + 32 * w + 8 * q + 4);
-          f[w][0] = u0.x; f[w][1] = u0.y; f[w][2] = u0.z; f[w][3] = u0.w;
-          f[w][4] = u1.x; f[w][5] = u1.y; f[w][6] = u1.z; f[w][7] = u1.w;
-        } else {
-          const uint4 u = *reinterpret_cast<const uint4 *>(from + 32 * w + 8 * q);
-          f[w][0] = lo_f(u.x); f[w][1] = hi_f(u.x); f[w][2] = lo_f(u.y); f[w][3] = hi_f(u.y);
-          f[w][4] = lo_f(u.z); f[w][5] = hi_f(u.z); f[w][6] = lo_f(u.w); f[w][7] = hi_f(u.w);
-        }
-#pragma unroll
-        for (int n = 0; n < 8; ++n) {
-          top = fmaxf(top, fabsf(f[w][n]));
-          bad |= !(fabsf(f[w][n]) <= 3.4028235e38f);
-        }
+        for (int k = 0; k < 4; ++k)
+          top = sizeof(T) == 4 ? max(top, x[k] & 0x7fffffffu) : __vmaxu2(top, x[k] & 0x7fff7fffu);
       }
-      top = fmaxf(top, __shfl_xor_sync(kAll, top, 1));
-      top = fmaxf(top, __shfl_xor_sync(kAll, top, 2));
-      bad = ((__ballot_sync(kAll, bad) >> (4 * g)) & 15u) != 0;
+      if (sizeof(T) == 2) top = max(top << 16, top & 0xffff0000u);
+      top = max(top, __shfl_xor_sync(kAll, top, 1));
+      top = max(top, __shfl_xor_sync(kAll, top, 2));
+      const bool bad = top >= 0x7f800000u;
       // q 2^-e with its largest in [2^14, 2^15): float16 keeps bfloat16 values exactly down to
       // 2^-31 of the largest, float32 ones to 22 bits in two pieces.  A row with an infinity or a
       // NaN is NaN.
-      int e = (int)((__float_as_uint(top) >> 23) & 255) - 127 - 14;
-      e = min(max(e, -114), 113);
+      const int e = min(max((int)(top >> 23) - 127 - 14, -114), 113);
       const float mul = bad ? CUDART_NAN_F : a.scale < 0.f ? -ldexpf(1.f, -e) : ldexpf(1.f, -e);
       // logits in units of log 2
       const float rfg = fmaxf(ldexpf(fabsf(a.scale) * 1.44269504f, e), 1e-37f);
+      const int row0 = sp.rb * C::kRows + rt * C::kTileRows + 8 * nb;
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         rf[nb][k] = __shfl_sync(kAll, rfg, (2 * q + k) * 4);
-        const int mm = (row0 + 2 * q + k) / a.G;
-        see[nb][k] = mm < rows ? min(max(len - rows + mm + 1, 0), len) : 0;
+        const int m = (row0 + 2 * q + k) / a.G;
+        see[nb][k] = m < sp.rows ? min(max(sp.len - sp.rows + m + 1, 0), sp.len) : 0;
         see_all = min(see_all, see[nb][k]);
       }
 #pragma unroll
       for (int w = 0; w < NGk; ++w) {
-        float hi[8], lo[8];
+        float u[8];
 #pragma unroll
         for (int n = 0; n < 8; ++n) {
-          const float u = f[w][n] * mul;
-          hi[n] = __half2float(__float2half_rn(u));
-          lo[n] = (u - hi[n]) * 2048.f;
+          const uint4 x = raw[nb][w * C::kLoads + (sizeof(T) == 4 ? n >> 2 : 0)];
+          const int k = sizeof(T) == 4 ? n & 3 : n >> 1;
+          const uint32_t y = k == 0 ? x.x : k == 1 ? x.y : k == 2 ? x.z : x.w;
+          u[n] = (sizeof(T) == 4 ? __uint_as_float(y) : n & 1 ? hi_f(y) : lo_f(y)) * mul;
         }
         // the two halves of a register of codes are nibbles n and n + 4
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          qb[0][nb][2 * w + k][0] = pack_f16(hi[2 * k], hi[2 * k + 4]);
-          qb[0][nb][2 * w + k][1] = pack_f16(hi[2 * k + 1], hi[2 * k + 5]);
-          if (QP == 2) {
-            qb[QP - 1][nb][2 * w + k][0] = pack_f16(lo[2 * k], lo[2 * k + 4]);
-            qb[QP - 1][nb][2 * w + k][1] = pack_f16(lo[2 * k + 1], lo[2 * k + 5]);
-          }
+        for (int n = 0; n < 4; ++n) {
+          const __half2 hi = __floats2half2_rn(u[n], u[n + 4]);
+          qb[0][nb][2 * w + (n >> 1)][n & 1] = bits(hi);
+          if (QP == 2)
+            qb[QP - 1][nb][2 * w + (n >> 1)][n & 1] =
+                pack_f16((u[n] - __low2float(hi)) * 2048.f, (u[n + 4] - __high2float(hi)) * 2048.f);
         }
       }
     }
@@ -525,8 +647,7 @@ attend(const AttendArgs a, const CacheView v, int *status) {
     float unit[NG];
     bool have_unit = false;
 
-    uint32_t used = 0;
-    int tok = (t0 + ts) * kTile - TS * kTile;
+    int tok = (sp.t0 + ts) * kTile - TS * kTile;
     for (int it = 0; it < n_it; ++it) {
       const uint8_t *tile = ring + used;
       used = used == (kStages - 1) * S::kBytes ? 0 : used + S::kBytes;
@@ -602,19 +723,19 @@ attend(const AttendArgs a, const CacheView v, int *status) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const float(&p)[4][2] = tk.p[nb];
-          float y = fmaxf(fmaxf(p[0][e], p[1][e]), fmaxf(p[2][e], p[3][e]));
-          y = fmaxf(y, __shfl_xor_sync(kAll, y, 4));
-          y = fmaxf(y, __shfl_xor_sync(kAll, y, 8));
-          y = fmaxf(y, __shfl_xor_sync(kAll, y, 16));
-          top[nb][e] = y * rf[nb][e];
-          move |= top[nb][e] > mx[nb][e] + 14.f;
+          top[nb][e] = fmaxf(fmaxf(p[0][e], p[1][e]), fmaxf(p[2][e], p[3][e]));
+          move |= top[nb][e] * rf[nb][e] > mx[nb][e] + 14.f;
         }
       if (__any_sync(kAll, move)) {
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const float now = fmaxf(mx[nb][e], top[nb][e] - 9.f);
+            float y = top[nb][e];
+            y = fmaxf(y, __shfl_xor_sync(kAll, y, 4));
+            y = fmaxf(y, __shfl_xor_sync(kAll, y, 8));
+            y = fmaxf(y, __shfl_xor_sync(kAll, y, 16));
+            const float now = fmaxf(mx[nb][e], y * rf[nb][e] - 9.f);
             const float fix = now == -CUDART_INF_F ? 1.f : ex2(mx[nb][e] - now);
             mx[nb][e] = now;
             l[nb][e] *= fix;
@@ -659,7 +780,7 @@ attend(const AttendArgs a, const CacheView v, int *status) {
           uint32_t big = 0;
 #pragma unroll
           for (int i = 0; i < 4; ++i)  // NaN is negative here, and left out
-            if (tok + 8 * i + g < len) big = __vmaxs2(big, ds[i][w]);
+            if (tok + 8 * i + g < sp.len) big = __vmaxs2(big, ds[i][w]);
           big = __vmaxs2(big, __shfl_xor_sync(kAll, big, 4));
           big = __vmaxs2(big, __shfl_xor_sync(kAll, big, 8));
           big = __vmaxs2(big, __shfl_xor_sync(kAll, big, 16));
@@ -695,140 +816,175 @@ attend(const AttendArgs a, const CacheView v, int *status) {
           values_f16<Dv, NB>(acc, tile + S::kV, ds, tk, lane);
       }
     }
-    cp_wait<0>();
-    __syncthreads();  // every slice is done with the ring: the sums go over it
-
-    // ---- the slices' sums, joined
-    float *sum = reinterpret_cast<float *>(smem);
+    // ---- the next span's queries are asked for, then the slices' sums joined, eight rows of
+    // every warp at a time
+    const int b = sp.b, hk = sp.hk, rb = sp.rb, rows = sp.rows;
+    const bool whole = sp.t0 == 0 && sp.t1 == sp.nt && !(C::kClusters && a.cluster);
+    const int slot = 2 * blockIdx.x + (spans ? 1 : 0);
+    if (sp.t0 == 0 && tid == 0 && !(C::kClusters && a.cluster))
+      a.ends[((int64_t)b * v.Hkv + hk) * a.nrb + rb] = make_int2(slot, blockIdx.x + sp.parts_in - 1);
+    const bool more = next_span(a, v, walk, sp, per);
+    if (more) load_rows(sp);
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb)
+    for (int nb = 0; nb < NB; ++nb) {
+      __syncthreads();  // the last sums have been read
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         float y = l[nb][e];
         y += __shfl_xor_sync(kAll, y, 4);
         y += __shfl_xor_sync(kAll, y, 8);
         y += __shfl_xor_sync(kAll, y, 16);
-        const int row = rt * C::kTileRows + 8 * nb + 2 * q + e;
+        const int row = rt * 8 + 2 * q + e;
         if (g == 0) {
           s_ml[ts][row][0] = mx[nb][e];
           s_ml[ts][row][1] = y;
         }
+        float *to = sum + (ts * RT * 8 + row) * C::kSumRow + g;
 #pragma unroll
         for (int j = 0; j < Dv / 16; ++j) {
           const float back = have_unit ? 1.f / unit[j >> 1] : 0.f;
-          float *to = sum + (ts * C::kRows + row) * C::kSumRow + 16 * j + g;
-          to[0] = acc.o[nb][j][e] * back;
-          to[8] = acc.o[nb][j][2 + e] * back;
+          to[16 * j] = acc.o[nb][j][e] * back;
+          to[16 * j + 8] = acc.o[nb][j][2 + e] * back;
         }
       }
-    __syncthreads();
-    const bool whole = t0 == 0 && t1 == nt;
-    const int slot = 2 * blockIdx.x + (x - (t1 - t0) == x0 ? 0 : 1);
-    for (int i = tid; i < C::kRows * (Dv / 4); i += kThreads) {
-      const int row = i / (Dv / 4), c = (i - row * (Dv / 4)) * 4;
-      const int gr = rb * C::kRows + row;
-      const int m = gr / a.G, h = hk * a.G + (gr - m * a.G);
-      if (m >= rows) continue;
-      float ref = -CUDART_INF_F;
+      __syncthreads();
+      for (int i = tid; i < RT * 8 * (Dv / 4); i += kThreads) {
+        const int r8 = i / (Dv / 4), c = (i - r8 * (Dv / 4)) * 4;
+        const int row = r8 / 8 * C::kTileRows + 8 * nb + r8 % 8;  // of the CTA
+        const int gr = rb * C::kRows + row;
+        const int m = gr / a.G, h = hk * a.G + (gr - m * a.G);
+        float ref = -CUDART_INF_F;
 #pragma unroll
-      for (int k = 0; k < TS; ++k) ref = fmaxf(ref, s_ml[k][row][0]);
-      const float at = ref == -CUDART_INF_F ? 0.f : ref;
-      float z = 0.f, y[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int k = 0; k < TS; ++k) ref = fmaxf(ref, s_ml[k][r8][0]);
+        const float at = ref == -CUDART_INF_F ? 0.f : ref;
+        float z = 0.f, y[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int k = 0; k < TS; ++k) {
-        const float f = ex2(s_ml[k][row][0] - at);
-        const float4 o = *reinterpret_cast<const float4 *>(sum + (k * C::kRows + row) * C::kSumRow + c);
-        z = fmaf(f, s_ml[k][row][1], z);
-        y[0] = fmaf(f, o.x, y[0]);
-        y[1] = fmaf(f, o.y, y[1]);
-        y[2] = fmaf(f, o.z, y[2]);
-        y[3] = fmaf(f, o.w, y[3]);
-      }
-      if (whole) {
-        const float inv = z == 0.f ? 0.f : 1.f / z;
-        T *dst = (T *)a.O.p + b * a.O.sb + h * a.O.sh + m * a.O.sn + c;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) st_elem(dst + e, y[e] * inv);
-        if (c == 0 && a.lse)
-          a.lse[((int64_t)b * a.H + h) * a.M + m] =
-              z == 0.f ? -CUDART_INF_F : (at + log2f(z)) * 0.693147181f;
-      } else {
-        const int64_t at_row = (int64_t)slot * C::kRows + row;
-        *reinterpret_cast<float4 *>(a.part + at_row * Dv + c) = make_float4(y[0], y[1], y[2], y[3]);
-        if (c == 0)
-          *reinterpret_cast<float2 *>(a.part_ml + at_row * 2) = make_float2(ref, z);
+        for (int k = 0; k < TS; ++k) {
+          const float f = ex2(s_ml[k][r8][0] - at);
+          const float4 o =
+              *reinterpret_cast<const float4 *>(sum + (k * RT * 8 + r8) * C::kSumRow + c);
+          z = fmaf(f, s_ml[k][r8][1], z);
+          y[0] = fmaf(f, o.x, y[0]);
+          y[1] = fmaf(f, o.y, y[1]);
+          y[2] = fmaf(f, o.z, y[2]);
+          y[3] = fmaf(f, o.w, y[3]);
+        }
+        if (whole) {
+          if (m < rows) finish_row<T>(a, b, h, m, c, y, z, at);
+        } else if (C::kClusters && a.cluster) {
+          float *to = reinterpret_cast<float *>(smem) + row * C::kSumRow;
+          *reinterpret_cast<float4 *>(to + c) = make_float4(y[0], y[1], y[2], y[3]);
+          if (c == 0) *reinterpret_cast<float4 *>(to + Dv) = make_float4(ref, z, 0.f, 0.f);
+        } else if (m < rows) {
+          const int64_t at_row = (int64_t)slot * C::kRows + row;
+          *reinterpret_cast<float4 *>(a.part + at_row * Dv + c) = make_float4(y[0], y[1], y[2], y[3]);
+          if (c == 0)
+            *reinterpret_cast<float2 *>(a.part_ml + at_row * 2) = make_float2(ref, z);
+        }
       }
     }
-    __syncthreads();  // the ring is free again
+    if (C::kClusters && a.cluster) {
+      // a row's sums of all CTAs of the cluster, the rows dealt out among them
+      cluster_sync();
+      const float *rows_at = reinterpret_cast<const float *>(smem);
+      for (int i = tid + kThreads * (blockIdx.x % a.cluster); i < C::kRows * (Dv / 4);
+           i += kThreads * a.cluster) {
+        const int row = i / (Dv / 4), c = (i - row * (Dv / 4)) * 4;
+        const int gr = rb * C::kRows + row;
+        const int m = gr / a.G, h = hk * a.G + (gr - m * a.G);
+        if (m >= rows) continue;
+        float ref = -CUDART_INF_F, z = 0.f, y[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int k = 0; k < a.cluster; ++k)
+          ref = fmaxf(ref, cluster_ld4(rows_at + row * C::kSumRow + Dv, k).x);
+        const float at = ref == -CUDART_INF_F ? 0.f : ref;
+        for (int k = 0; k < a.cluster; ++k) {
+          const float4 ml = cluster_ld4(rows_at + row * C::kSumRow + Dv, k);
+          const float4 o = cluster_ld4(rows_at + row * C::kSumRow + c, k);
+          const float f = ex2(ml.x - at);
+          z = fmaf(f, ml.y, z);
+          y[0] = fmaf(f, o.x, y[0]);
+          y[1] = fmaf(f, o.y, y[1]);
+          y[2] = fmaf(f, o.z, y[2]);
+          y[3] = fmaf(f, o.w, y[3]);
+        }
+        finish_row<T>(a, b, h, m, c, y, z, at);
+      }
+      cluster_sync();  // the others may still be reading
+    }
+    if (!more) break;
   }
+  cp_wait<0>();
 }
 
-// Rows of items that lie in several stretches (or in none: nothing to see).  One CTA per row:
-// its four warps take the stretches in turn, and their sums are joined in a fixed order.
+// Rows of items that lie in several stretches (or in none: nothing to see).  One CTA per row: the
+// weights of all parts first, then their sums by four warps in turn, all loads independent, joined
+// in a fixed order.
 template <typename T, int Dv, int kRows>
-__global__ void __launch_bounds__(128) attend_join(const AttendArgs a, const CacheView v, int ctas,
+__global__ void __launch_bounds__(128) attend_join(const AttendArgs a, const CacheView v,
                                                    int *status) {
-  __shared__ int64_t run[128 + 4];
-  __shared__ float s_m[4], s_l[4], s_o[4][Dv];
+  constexpr int kThreads = 128, kGroups = kThreads / (Dv / 4);
+  __shared__ float s_w[kMaxCtas], s_red[8];
+  __shared__ float4 s_y[kGroups][Dv / 4];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int gr = blockIdx.x, hk = blockIdx.y, b = blockIdx.z;
   const int rows = seq_rows(a, b);
-  if (gr == 0 && hk == 0 && tid == 0) {
-    if (a.counts && rows != a.counts[b]) report(status, MUSE_ERR_DEVICE);
-    if (seq_len(a, v, b) != a.lens[b]) report(status, MUSE_ERR_DEVICE);
-  }
+  if (gr == 0 && hk == 0 && tid == 0) check_lengths(a, v, b, status);
   const int m = gr / a.G, h = hk * a.G + (gr - m * a.G);
   const int nt = m < rows ? seq_tiles(a, v, b) : 0;
-  float ref = -CUDART_INF_F, z = 0.f;
-  float y[Dv / 32];
-#pragma unroll
-  for (int e = 0; e < Dv / 32; ++e) y[e] = 0.f;
-  const int rb = gr / kRows, row = gr - rb * kRows;
-  int64_t c0 = 0, c1 = -1, per = 1, start = 0;
-  if (nt) {
-    const int64_t total = line_total<128>(a, v, run);
-    per = stretch(total, ctas, a.min_tiles);
-    // position of sequence b's first tile
-    const int pb = (a.B + 127) / 128, own = b / pb;
-    int64_t first = own ? run[own - 1] : 0;
-    for (int i = own * pb; i < b; ++i) first += (int64_t)seq_tiles(a, v, i) * v.Hkv * a.nrb;
-    start = first + (int64_t)(hk * a.nrb + rb) * nt;
-    c0 = start / per;
-    c1 = (start + nt - 1) / per;
-  }
   asm volatile("griddepcontrol.wait;" ::: "memory");  // on every path: attend ends before this
-  if (m >= rows || c0 == c1) return;                   // finished by its only CTA
-  for (int64_t c = c0 + warp; c <= c1; c += 4) {
-    const int64_t slot = (2 * c + (start <= c * per ? 0 : 1)) * kRows + row;
-    const float2 ml = *reinterpret_cast<const float2 *>(a.part_ml + slot * 2);
-    const float now = fmaxf(ref, ml.x), at = now == -CUDART_INF_F ? 0.f : now;
-    const float fa = ex2(ref - at), fb = ex2(ml.x - at);
-    ref = now;
-    z = z * fa + ml.y * fb;
-#pragma unroll
-    for (int e = 0; e < Dv / 32; ++e) y[e] = y[e] * fa + a.part[slot * Dv + 32 * e + lane] * fb;
+  if (m >= rows) return;
+  const int rb = gr / kRows, row = gr - rb * kRows;
+  const int64_t item = ((int64_t)b * v.Hkv + hk) * a.nrb + rb;
+  const int2 ends = nt ? a.ends[item] : make_int2(0, -1);
+  const int c0 = ends.x >> 1, n = ends.y - c0 + 1;
+  if (n == 1) return;  // finished by its only CTA
+  // a part that begins its stretch is in the even slot: all but, perhaps, the first
+  auto slot_of = [&](int k) { return k ? 2 * (int64_t)(c0 + k) : (int64_t)ends.x; };
+  float ref = -CUDART_INF_F;
+  for (int k = tid; k < n; k += kThreads) {
+    const int64_t slot = slot_of(k);
+    s_w[k] = a.part_ml[(slot * kRows + row) * 2];
+    ref = fmaxf(ref, s_w[k]);
   }
-  if (lane == 0) {
-    s_m[warp] = ref;
-    s_l[warp] = z;
-  }
-#pragma unroll
-  for (int e = 0; e < Dv / 32; ++e) s_o[warp][32 * e + lane] = y[e];
+  ref = warp_max(ref);
+  if (lane == 0) s_red[warp] = ref;
   __syncthreads();
-  float top = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3]));
-  const float at = top == -CUDART_INF_F ? 0.f : top;
-  float zz = 0.f, o = 0.f;
-#pragma unroll
-  for (int w = 0; w < 4; ++w) {
-    const float f = ex2(s_m[w] - at);
-    zz = fmaf(f, s_l[w], zz);
-    if (tid < Dv) o = fmaf(f, s_o[w][tid], o);
+  ref = fmaxf(fmaxf(s_red[0], s_red[1]), fmaxf(s_red[2], s_red[3]));
+  const float at = ref == -CUDART_INF_F ? 0.f : ref;
+  float z = 0.f;
+  for (int k = tid; k < n; k += kThreads) {
+    const int64_t slot = slot_of(k);
+    s_w[k] = ex2(s_w[k] - at);
+    z = fmaf(s_w[k], a.part_ml[(slot * kRows + row) * 2 + 1], z);
   }
-  if (tid < Dv)
-    st_elem((T *)a.O.p + b * a.O.sb + h * a.O.sh + m * a.O.sn + tid, zz == 0.f ? 0.f : o / zz);
-  if (tid == 0 && a.lse)
-    a.lse[((int64_t)b * a.H + h) * a.M + m] =
-        zz == 0.f ? -CUDART_INF_F : (at + log2f(zz)) * 0.693147181f;
+  z = warp_sum(z);
+  if (lane == 0) s_red[4 + warp] = z;
+  __syncthreads();
+  z = (s_red[4] + s_red[5]) + (s_red[6] + s_red[7]);
+  const int grp = tid / (Dv / 4), c4 = tid - grp * (Dv / 4);
+  float y[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
+  for (int k = grp; k < n; k += kGroups) {
+    const int64_t slot = slot_of(k);
+    const float4 o = reinterpret_cast<const float4 *>(a.part + (slot * kRows + row) * Dv)[c4];
+    const float f = s_w[k];
+    y[0] = fmaf(f, o.x, y[0]);
+    y[1] = fmaf(f, o.y, y[1]);
+    y[2] = fmaf(f, o.z, y[2]);
+    y[3] = fmaf(f, o.w, y[3]);
+  }
+  s_y[grp][c4] = make_float4(y[0], y[1], y[2], y[3]);
+  __syncthreads();
+  if (grp) return;
+#pragma unroll
+  for (int k = 1; k < kGroups; ++k) {
+    const float4 o = s_y[k][c4];
+    y[0] += o.x;
+    y[1] += o.y;
+    y[2] += o.z;
+    y[3] += o.w;
+  }
+  finish_row<T>(a, b, h, m, 4 * c4, y, z, at);
 }
 
 // Rows of a CTA: 8, 16, 32 or blocks of 64 (a warp takes 8 or 16).
@@ -858,23 +1014,37 @@ cudaError_t launch(AttendArgs a, const CacheView &v, int *status, cudaStream_t s
   const int rows = a.G * a.M;
   a.nrb = (rows + C::kRows - 1) / C::kRows;
   a.min_tiles = C::kSlices;
-  // no more CTAs than the table could hold stretches for
-  const int64_t most = (int64_t)a.B * v.Hkv * a.nrb * (((int64_t)v.max_pages << v.page_log2) / kTile);
-  const int ctas = (int)std::min<int64_t>(fit, (most + a.min_tiles - 1) / a.min_tiles);
-  kernel<<<ctas, 32 * kWarps, C::kSmem, st>>>(a, v, status);
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
+  const int64_t items = (int64_t)a.B * v.Hkv * a.nrb;
+  const int64_t cap = ((int64_t)v.max_pages << v.page_log2) / kTile;  // tiles a sequence can have
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(rows, v.Hkv, a.B);
-  cfg.blockDim = dim3(128);
+  cfg.blockDim = dim3(32 * kWarps);
+  cfg.dynamicSmemBytes = C::kSmem;
   cfg.stream = st;
   cudaLaunchAttribute at[1];
+  cfg.attrs = at;
+  if (C::kClusters && cap <= kClusterTiles * C::kSlices && items * kCluster <= 2 * fit) {
+    a.cluster = (int)std::max<int64_t>(1, std::min<int64_t>(kCluster, (cap + C::kSlices - 1) / C::kSlices));
+    cfg.gridDim = dim3((unsigned)(items * a.cluster));
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = a.cluster;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.numAttrs = 1;
+    count_launches(1);
+    return cudaLaunchKernelEx(&cfg, kernel, a, v, status);
+  }
+  // no more CTAs than the table could hold stretches for
+  const int ctas = (int)std::min<int64_t>(fit, (items * cap + a.min_tiles - 1) / a.min_tiles);
+  cfg.gridDim = dim3(ctas);
+  e = cudaLaunchKernelEx(&cfg, kernel, a, v, status);
+  if (e != cudaSuccess) return e;
+  cfg.gridDim = dim3(rows, v.Hkv, a.B);
+  cfg.blockDim = dim3(128);
+  cfg.dynamicSmemBytes = 0;
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
   cfg.numAttrs = 1;
   count_launches(2);
-  return cudaLaunchKernelEx(&cfg, attend_join<T, Dv, C::kRows>, a, v, ctas, status);
+  return cudaLaunchKernelEx(&cfg, attend_join<T, Dv, C::kRows>, a, v, status);
 }
 
 template <typename T, int D, int Dv>
@@ -887,6 +1057,17 @@ cudaError_t by_rows(const AttendArgs &a, const CacheView &v, int *status, cudaSt
   }
 }
 
+// Partial sums and references of two parts a CTA, and the ends of every item.
+struct AttendWs {
+  size_t part, part_ml, ends;
+  AttendWs(int64_t B, int64_t H, int64_t M, int64_t Dv, int64_t Hkv) {
+    const int64_t all = H / Hkv * M, rows = block_rows((int)std::min<int64_t>(all, 1 << 20));
+    part = align_up((size_t)(2 * kMaxCtas * rows * Dv * 4));
+    part_ml = align_up((size_t)(2 * kMaxCtas * rows * 8));
+    ends = align_up((size_t)(B * Hkv * ((all + rows - 1) / rows) * 8));
+  }
+};
+
 template <typename T>
 cudaError_t by_width(const AttendArgs &a, const muse_dims &d, const CacheView &v, int *status,
                      cudaStream_t st) {
@@ -898,8 +1079,8 @@ cudaError_t by_width(const AttendArgs &a, const muse_dims &d, const CacheView &v
 }  // namespace
 
 size_t cache_attend_ws(const muse_dims &d, int Hkv) {
-  const size_t rows = block_rows(d.H / Hkv * d.N);
-  return align_up((size_t)2 * kMaxCtas * rows * d.Dv * 4) + align_up((size_t)2 * kMaxCtas * rows * 8);
+  const AttendWs w(d.B, d.H, d.N, d.Dv, Hkv);
+  return w.part + w.part_ml + w.ends;
 }
 
 cudaError_t run_cache_attend(const muse_rows &Q, const muse_dims &d, const muse_cache &c,
@@ -915,12 +1096,13 @@ cudaError_t run_cache_attend(const muse_rows &Q, const muse_dims &d, const muse_
   a.H = d.H;
   a.M = d.N;
   a.G = d.H / c.Hkv;
-  a.nrb = a.min_tiles = 0;
+  a.nrb = a.min_tiles = a.cluster = 0;
   a.scale = d.scale;
-  const size_t rows = block_rows(a.G * a.M);
-  a.part = static_cast<float *>(ws);
-  a.part_ml = reinterpret_cast<float *>(static_cast<char *>(ws) +
-                                        align_up((size_t)2 * kMaxCtas * rows * d.Dv * 4));
+  const AttendWs w(d.B, d.H, d.N, d.Dv, c.Hkv);
+  char *p = static_cast<char *>(ws);
+  a.part = reinterpret_cast<float *>(p);
+  a.part_ml = reinterpret_cast<float *>(p + w.part);
+  a.ends = reinterpret_cast<int2 *>(p + w.part + w.part_ml);
   const CacheView v = cache_view(c);
   return d.dtype == MUSE_F32 ? by_width<float>(a, d, v, status, st)
                              : by_width<__nv_bfloat16>(a, d, v, status, st);

@@ -410,6 +410,11 @@ _CODE = {torch.float32: MUSE_F32, torch.bfloat16: MUSE_BF16}
 
 
 @functools.lru_cache(maxsize=4096)
+def _dims7(B, H, N, D, Dv, code, scale=1.0) -> MuseDims:
+    return MuseDims(B, H, N, D, Dv, code, scale)
+
+
+@functools.lru_cache(maxsize=4096)
 def _layout(shape, stride, dtype, written: bool):
     """(sb, sh, sn) of rows [B,H,N,D] of this geometry, or what is wrong with it; a dimension of
     size 1 has no stride of its own."""
@@ -484,7 +489,7 @@ def muse_rope_axes(Q, positions, sections, base: float = 10000.0, K=None, flags:
     nb = 1 if positions.dim() == 2 else B
     pos = _ints(positions, (axes, N) if positions.dim() == 2 else (B, axes, N), "positions", dev)
     if out is None:
-        out = torch.empty((B, H, N, D), dtype=Q.dtype, device=Q.device)
+        out = Q.new_empty((B, H, N, D))
     else:
         _four(out, "out", Q.shape, Q)
         _same_place(Q, out, "out")
@@ -493,12 +498,12 @@ def muse_rope_axes(Q, positions, sections, base: float = 10000.0, K=None, flags:
         Hk = K.shape[1] if K.dim() == 4 else 0
         _four(K, "K", (B, Hk, N, D), Q)
         if k_out is None:
-            k_out = torch.empty((B, Hk, N, D), dtype=Q.dtype, device=Q.device)
+            k_out = Q.new_empty((B, Hk, N, D))
         else:
             _four(k_out, "k_out", K.shape, Q)
             _same_place(K, k_out, "k_out")
         k, ko = _rows(K, "K"), _rows(k_out, "k_out", True)
-    _call("muse_rope_axes", dev, _rows(Q, "Q"), k, Hk, MuseDims(B, H, N, D, D, code, 1.0), pos, nb,
+    _call("muse_rope_axes", dev, _rows(Q, "Q"), k, Hk, _dims7(B, H, N, D, D, code), pos, nb,
           _rope(tuple(sections), float(base), flags), _rows(out, "out", True), ko)
     return out if K is None else (out, k_out)
 
@@ -555,7 +560,7 @@ def muse_cache_write(cache, K, V, page_table, start, counts=None):
     if H != c.Hkv:
         raise ValueError(f"K: shape {tuple(K.shape)}, the cache has {c.Hkv} heads")
     _four(V, "V", (B, H, N, Dv), K)
-    _call("muse_cache_write", dev, _rows(K, "K"), _rows(V, "V"), MuseDims(B, H, N, D, Dv, code, 1.0), c,
+    _call("muse_cache_write", dev, _rows(K, "K"), _rows(V, "V"), _dims7(B, H, N, D, Dv, code), c,
           _ints(start, (B,), "start", dev), _ints(counts, (B,), "counts", dev))
     return cache
 
@@ -569,9 +574,8 @@ def muse_cache_read(cache, page_table, start, N: int, D: int, dtype=torch.bfloat
     if out is None:
         if dtype not in _CODE:
             raise ValueError(f"dtype: expected float32 or bfloat16, got {dtype}")
-        new = torch.empty if counts is None else torch.zeros
-        K = new((B, c.Hkv, N, D), dtype=dtype, device=cache.device)
-        V = new((B, c.Hkv, N, Dv), dtype=dtype, device=cache.device)
+        new = cache.new_empty if counts is None else cache.new_zeros
+        K, V = new((B, c.Hkv, N, D), dtype=dtype), new((B, c.Hkv, N, Dv), dtype=dtype)
     else:
         K, V = out
         _first(K, "K")
@@ -579,7 +583,7 @@ def muse_cache_read(cache, page_table, start, N: int, D: int, dtype=torch.bfloat
             raise ValueError(f"K: on {K.device}, the cache on {cache.device}")
         _four(K, "K", (B, c.Hkv, N, D), K)
         _four(V, "V", (B, c.Hkv, N, Dv), K)
-    _call("muse_cache_read", dev, MuseDims(B, c.Hkv, N, D, Dv, _CODE[K.dtype], 1.0), c,
+    _call("muse_cache_read", dev, _dims7(B, c.Hkv, N, D, Dv, _CODE[K.dtype]), c,
           _ints(start, (B,), "start", dev), _ints(counts, (B,), "counts", dev),
           _rows(K, "K", True), _rows(V, "V", True))
     return K, V
@@ -595,17 +599,17 @@ def muse_cache_attend(Q, cache, page_table, lens, counts=None, scale: float = 1.
     (B, H, N, D), code = _first(Q, "Q")
     dev = Q.get_device()
     c, Dv = _cache(cache, page_table, B, D, dev)
-    new = torch.empty if counts is None else torch.zeros
+    new = Q.new_empty if counts is None else Q.new_zeros
     if out is None:
-        out = new((B, H, N, Dv), dtype=Q.dtype, device=Q.device)
+        out = new((B, H, N, Dv))
     else:
         _four(out, "out", (B, H, N, Dv), Q)
     if lse is None:
-        lse = new((B, H, N), dtype=torch.float32, device=Q.device)
+        lse = new((B, H, N), dtype=torch.float32)
     elif lse.shape != (B, H, N) or lse.dtype != torch.float32 or not lse.is_contiguous() \
             or lse.get_device() != dev:
         raise ValueError(f"lse: expected a contiguous float32 tensor {[B, H, N]} on {Q.device}")
-    d = MuseDims(B, H, N, D, Dv, code, scale)
+    d = _dims7(B, H, N, D, Dv, code, scale)
     if ws is None:
         ws = workspace("muse_cache_attend", d, c.Hkv, device=Q.device)
     elif ws.dtype != torch.uint8 or not ws.is_contiguous() or ws.get_device() != dev:
