@@ -146,6 +146,8 @@ __global__ void __launch_bounds__(D + Dv) cache_write(const CacheRows a, const C
   constexpr int kThreads = D + Dv;
   __shared__ __align__(16) uint32_t img[S::kBytes / 4];
   const int b = blockIdx.z, h = blockIdx.y, tid = threadIdx.x;
+  dependents_may_launch();
+  wait_for_earlier();
   const int count = row_count(a.counts, b, a.N, status);
   const int start = a.start[b];
   // tiles are counted from the one that holds the first token (rounded down for start < 0)
@@ -221,6 +223,8 @@ __global__ void __launch_bounds__(D + Dv) cache_read(const CacheRows a, const Ca
   constexpr int kThreads = D + Dv;
   __shared__ __align__(16) uint32_t img[S::kBytes / 4];
   const int b = blockIdx.z, h = blockIdx.y, tid = threadIdx.x;
+  dependents_may_launch();
+  wait_for_earlier();
   const int count = row_count(a.counts, b, a.N, status);
   const int start = a.start[b];
   const int64_t tile = (int64_t)(start >> 5) + blockIdx.x;
@@ -265,10 +269,9 @@ cudaError_t launch(bool write, const CacheRows &a, const CacheView &v, int B, in
                    cudaStream_t st) {
   // N rows from any start touch at most (N + 30) / 32 + 1 tiles
   const dim3 grid((unsigned)((a.N + 30) / 32 + 1), (unsigned)v.Hkv, (unsigned)B);
-  if (write) cache_write<T, D, Dv><<<grid, D + Dv, 0, st>>>(a, v, status);
-  else cache_read<T, D, Dv><<<grid, D + Dv, 0, st>>>(a, v, status);
-  count_launches(1);
-  return cudaGetLastError();
+  return launch_next(write ? cache_write<T, D, Dv> : cache_read<T, D, Dv>, grid, D + Dv, 0, st, true, 0, a,
+                     v,
+                     status);
 }
 
 template <typename T>

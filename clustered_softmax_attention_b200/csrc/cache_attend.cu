@@ -469,7 +469,8 @@ attend(const __grid_constant__ AttendArgs a, const __grid_constant__ CacheView v
   Walk walk;
   Span sp;
   int64_t per = 1;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  dependents_may_launch();
+  wait_for_earlier();
   if (C::kClusters && a.cluster) {
     const int rank = blockIdx.x % a.cluster, item = blockIdx.x / a.cluster;
     sp.b = item / (v.Hkv * a.nrb);
@@ -657,7 +658,7 @@ attend(const __grid_constant__ AttendArgs a, const __grid_constant__ CacheView v
       fetch();
       const bool here = there & 1u;
       there >>= 1;
-      if (!here) continue;
+      if (__builtin_expect(!here, 0)) continue;
 
       // ---- logits
       Tok<NB> tk;
@@ -706,7 +707,7 @@ attend(const __grid_constant__ AttendArgs a, const __grid_constant__ CacheView v
       for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
         for (int e = 0; e < 2; ++e) hide.left[nb][e] = see[nb][e] - tok;
-      if (hide.edge) {
+      if (__builtin_expect(hide.edge, 0)) {
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -726,7 +727,7 @@ attend(const __grid_constant__ AttendArgs a, const __grid_constant__ CacheView v
           top[nb][e] = fmaxf(fmaxf(p[0][e], p[1][e]), fmaxf(p[2][e], p[3][e]));
           move |= top[nb][e] * rf[nb][e] > mx[nb][e] + 14.f;
         }
-      if (__any_sync(kAll, move)) {
+      if (__builtin_expect(__any_sync(kAll, move), 0)) {
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -753,7 +754,7 @@ attend(const __grid_constant__ AttendArgs a, const __grid_constant__ CacheView v
 #pragma unroll
           for (int e = 0; e < 2; ++e)
             tk.p[nb][i][e] = ex2(fmaf(tk.p[nb][i][e], rf[nb][e], -mx[nb][e]));
-      if (hide.edge) {
+      if (__builtin_expect(hide.edge, 0)) {
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -773,7 +774,7 @@ attend(const __grid_constant__ AttendArgs a, const __grid_constant__ CacheView v
       uint32_t ds[4][NG / 2];
 #pragma unroll
       for (int i = 0; i < 4; ++i) steps<Dv>(tile + S::kVStep, 8 * i + g, ds[i]);
-      if (!have_unit) {
+      if (__builtin_expect(!have_unit, 0)) {
         have_unit = true;
 #pragma unroll
         for (int w = 0; w < NG / 2; ++w) {
@@ -810,7 +811,7 @@ attend(const __grid_constant__ AttendArgs a, const __grid_constant__ CacheView v
             off_range |= ds[i][w] ^ 0x04000400u;
             ds[i][w] <<= 3;
           }
-        if (__any_sync(kAll, off_range & 0xfc00fc00u))
+        if (__builtin_expect(__any_sync(kAll, off_range & 0xfc00fc00u), 0))
           values_wide<Dv, NB, 2>(acc, tile + S::kV, tile + S::kVStep, tk, unit, hide, lane);
         else
           values_f16<Dv, NB>(acc, tile + S::kV, ds, tk, lane);
@@ -927,11 +928,12 @@ __global__ void __launch_bounds__(128) attend_join(const AttendArgs a, const Cac
   __shared__ float4 s_y[kGroups][Dv / 4];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int gr = blockIdx.x, hk = blockIdx.y, b = blockIdx.z;
+  dependents_may_launch();
+  wait_for_earlier();
   const int rows = seq_rows(a, b);
   if (gr == 0 && hk == 0 && tid == 0) check_lengths(a, v, b, status);
   const int m = gr / a.G, h = hk * a.G + (gr - m * a.G);
   const int nt = m < rows ? seq_tiles(a, v, b) : 0;
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // on every path: attend ends before this
   if (m >= rows) return;
   const int rb = gr / kRows, row = gr - rb * kRows;
   const int64_t item = ((int64_t)b * v.Hkv + hk) * a.nrb + rb;
@@ -1016,35 +1018,17 @@ cudaError_t launch(AttendArgs a, const CacheView &v, int *status, cudaStream_t s
   a.min_tiles = C::kSlices;
   const int64_t items = (int64_t)a.B * v.Hkv * a.nrb;
   const int64_t cap = ((int64_t)v.max_pages << v.page_log2) / kTile;  // tiles a sequence can have
-  cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(32 * kWarps);
-  cfg.dynamicSmemBytes = C::kSmem;
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  cfg.attrs = at;
   if (C::kClusters && cap <= kClusterTiles * C::kSlices && items * kCluster <= 2 * fit) {
     a.cluster = (int)std::max<int64_t>(1, std::min<int64_t>(kCluster, (cap + C::kSlices - 1) / C::kSlices));
-    cfg.gridDim = dim3((unsigned)(items * a.cluster));
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = a.cluster;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    cfg.numAttrs = 1;
-    count_launches(1);
-    return cudaLaunchKernelEx(&cfg, kernel, a, v, status);
+    return launch_next(kernel, dim3((unsigned)(items * a.cluster)), 32 * kWarps, C::kSmem, st,
+                       true, a.cluster, a, v, status);
   }
   // no more CTAs than the table could hold stretches for
   const int ctas = (int)std::min<int64_t>(fit, (items * cap + a.min_tiles - 1) / a.min_tiles);
-  cfg.gridDim = dim3(ctas);
-  e = cudaLaunchKernelEx(&cfg, kernel, a, v, status);
+  e = launch_next(kernel, dim3(ctas), 32 * kWarps, C::kSmem, st, false, 0, a, v, status);
   if (e != cudaSuccess) return e;
-  cfg.gridDim = dim3(rows, v.Hkv, a.B);
-  cfg.blockDim = dim3(128);
-  cfg.dynamicSmemBytes = 0;
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.numAttrs = 1;
-  count_launches(2);
-  return cudaLaunchKernelEx(&cfg, attend_join<T, Dv, C::kRows>, a, v, status);
+  return launch_next(attend_join<T, Dv, C::kRows>, dim3(rows, v.Hkv, a.B), 128, 0, st, true, 0, a, v,
+                     status);
 }
 
 template <typename T, int D, int Dv>

@@ -181,6 +181,34 @@ cudaError_t run_diag_merge(const void *Q, const void *K, const void *V, int dtyp
 // Serving: rotary positions (rope.cu), the 4-bit cache (cache.cu), attention over it
 // (cache_attend.cu).  Arguments are validated in serving_api.cu.
 // ---------------------------------------------------------------------------
+// A serving kernel's launch: it may be made resident while the kernel before it on the stream still
+// runs (the gap between two small kernels is as long as they are), and waits for that one's end
+// (wait_for_earlier) before it touches memory.  early = false: it starts on an empty card, as a
+// grid that fills it exactly has to.  cluster: CTAs of a cluster, or 0.
+template <typename... P, typename... A>
+cudaError_t launch_next(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st,
+                        bool early, int cluster, const A &...args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[2];
+  cfg.attrs = at;
+  if (early) {
+    at[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
+  }
+  if (cluster) {
+    at[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+    at[cfg.numAttrs].val.clusterDim.x = cluster;
+    at[cfg.numAttrs].val.clusterDim.y = at[cfg.numAttrs].val.clusterDim.z = 1;
+    ++cfg.numAttrs;
+  }
+  count_launches(1);
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // Phase table of a muse_rope: pair i turns by pos * turn[i] / 2^64 of a turn.
 struct RopeTable {
   int P;           // pairs

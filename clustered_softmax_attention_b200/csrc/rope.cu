@@ -86,6 +86,8 @@ constexpr int kHeads = 4;  // heads whose loads are under way together
 template <typename T, int D, int VEC, bool ADJ>
 __global__ void __launch_bounds__(kThreads) rope(const RopeArgs a, const __grid_constant__ RopeTable t) {
   constexpr int kRow = D / (2 * VEC);  // threads of a row
+  dependents_may_launch();
+  wait_for_earlier();
   const int64_t id = (int64_t)blockIdx.x * kThreads + threadIdx.x;
   const int64_t row = id / kRow;
   const int u = (int)(id - row * kRow);
@@ -164,9 +166,8 @@ cudaError_t launch(RopeArgs a, const RopeTable &t, cudaStream_t st) {
   const int64_t split = std::max<int64_t>(1, std::min<int64_t>(heads, (148 * 8 + ctas - 1) / ctas));
   a.heads_per_cta = (int)((heads + split - 1) / split);
   const unsigned groups = (unsigned)((heads + a.heads_per_cta - 1) / a.heads_per_cta);
-  rope<T, D, VEC, ADJ><<<dim3((unsigned)ctas, groups), kThreads, 0, st>>>(a, t);
-  count_launches(1);
-  return cudaGetLastError();
+  return launch_next(rope<T, D, VEC, ADJ>, dim3((unsigned)ctas, groups), kThreads, 0, st, true, 0,
+                     a, t);
 }
 
 template <typename T, int D>
