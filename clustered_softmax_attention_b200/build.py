@@ -1,4 +1,5 @@
-"""Build step: compiles csrc/*.cu for sm_100a into libmuse.so next to this file.
+"""Build step: compiles csrc/*.cu for sm_100a into libmuse.so next to this file, and
+csrc/binding.cpp (the CPython binding of the serving entry points) into _serving.so beside it.
 
 Run as ``python -m clustered_softmax_attention_b200.build`` (or through
 ``__graft_entry__.build()``).  nvcc cross-compiles, so no GPU is needed.
@@ -16,6 +17,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 OUT = os.path.join(PKG, "libmuse.so")
+BINDING = os.path.join(PKG, "_serving.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -72,7 +74,33 @@ def build(verbose: bool = False, ptxas_info: bool = False, force: bool = False) 
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode:
             raise RuntimeError("link failed:\n" + r.stdout + r.stderr)
+    _build_binding(verbose, force)
     return OUT
+
+
+def _build_binding(verbose: bool, force: bool) -> None:
+    """csrc/binding.cpp against this interpreter and its torch, linked to libmuse.so."""
+    src = os.path.join(CSRC, "binding.cpp")
+    if not force and not _stale(BINDING, src, [os.path.join(ROOT, "include", "muse.h")]):
+        return
+    import sysconfig
+
+    import torch
+    from torch.utils.cpp_extension import include_paths, library_paths
+
+    cuda = os.path.dirname(os.path.dirname(_nvcc()))
+    dirs = [os.path.join(ROOT, "include"), sysconfig.get_paths()["include"], *include_paths(),
+            os.path.join(cuda, "include")]
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-w",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *(f"-I{d}" for d in dirs), src, "-o", BINDING, *(f"-L{d}" for d in library_paths()),
+           "-L" + PKG, "-l:libmuse.so", "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10",
+           "-lc10_cuda", "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if verbose or r.returncode:
+        sys.stderr.write(" ".join(cmd) + "\n" + r.stdout + r.stderr)
+    if r.returncode:
+        raise RuntimeError("the binding did not build")
 
 
 if __name__ == "__main__":

@@ -3,13 +3,14 @@
 Every function here has the name of the C entry point it calls (include/muse.h)
 and does nothing but check shapes, allocate the caller-owned outputs and
 workspace with torch, and pass device pointers plus the current CUDA stream.
+The serving entry points (the last section) do so in a compiled module.
 All arithmetic runs in the library's CUDA kernels; if the library is missing,
 the import of this module fails loudly.
 """
 from __future__ import annotations
 
 import ctypes
-import functools
+import importlib.util
 import os
 import re
 from typing import Optional
@@ -399,81 +400,31 @@ def muse_backward(Q, K, V, dO, q_perm, q_offsets, k_perm, k_offsets, scale: floa
 # Serving: rotary positions, the 4-bit cache, attention over it.
 #
 # These take rows as they lie (any batch, head and row strides that are multiples of 16 bytes,
-# the last dimension dense) and run on the current stream of the tensors' device.
+# the last dimension dense) and run on the current stream of the tensors' device.  They are called
+# once a token, so their marshalling is compiled (csrc/binding.cpp -> _serving.so): the same
+# checks, a few microseconds less.
 # ---------------------------------------------------------------------------------------
 MUSE_ROPE_INVERSE = 1
 MUSE_ROPE_ADJACENT = 2
 MUSE_ROPE_AXIS_LADDER = 4
 MUSE_CACHE_MAX_ROWS = 128
-_ITEM = {torch.float32: 4, torch.bfloat16: 2}
-_CODE = {torch.float32: MUSE_F32, torch.bfloat16: MUSE_BF16}
+
+_SERVING = None
 
 
-@functools.lru_cache(maxsize=4096)
-def _dims7(B, H, N, D, Dv, code, scale=1.0) -> MuseDims:
-    return MuseDims(B, H, N, D, Dv, code, scale)
-
-
-@functools.lru_cache(maxsize=4096)
-def _layout(shape, stride, dtype, written: bool):
-    """(sb, sh, sn) of rows [B,H,N,D] of this geometry, or what is wrong with it; a dimension of
-    size 1 has no stride of its own."""
-    sb, sh, sn = (st if n > 1 else 0 for n, st in zip(shape[:3], stride[:3]))
-    if stride[3] != 1 or (sb | sh | sn) % (16 // _ITEM[dtype]):
-        return f"rows must be dense and 16-byte aligned, strides {tuple(stride)}"
-    if written:
-        end = shape[3]  # rows that are written must not overlap: each stride clears those below
-        for st, n in sorted((st, n) for st, n in zip((sb, sh, sn), shape) if n > 1):
-            if st < end:
-                return f"overlapping rows, strides {tuple(stride)}"
-            end += st * (n - 1)
-    return sb, sh, sn
-
-
-def _rows(t: torch.Tensor, name: str, written: bool = False) -> MuseRows:
-    """The view of a [B,H,N,D] tensor on the GPU."""
-    if not t.is_cuda:
-        raise ValueError(f"{name}: expected a CUDA tensor")
-    at, p = _layout(t.shape, t.stride(), t.dtype, written), t.data_ptr()
-    if at.__class__ is str or p & 15:
-        raise ValueError(f"{name}: {at if at.__class__ is str else 'rows must be 16-byte aligned'}")
-    return MuseRows(p, *at)
-
-
-def _ints(t: Optional[torch.Tensor], shape, name: str, dev: int) -> Optional[int]:
-    if t is None:
-        return None
-    if t.shape != shape or t.dtype != torch.int32 or not t.is_contiguous() or t.get_device() != dev:
-        raise ValueError(f"{name}: expected a contiguous int32 tensor {list(shape)} on the GPU of the "
-                         f"other arguments, got {t.dtype} {list(t.shape)} on {t.device}")
-    return t.data_ptr()
-
-
-def _four(t: torch.Tensor, name: str, shape, like: torch.Tensor):
-    if t.shape != shape:
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.dtype != like.dtype or t.get_device() != like.get_device():
-        raise ValueError(f"{name}: {t.dtype} on {t.device}, expected {like.dtype} on {like.device}")
-
-
-def _first(t: torch.Tensor, name: str):
-    """Shape and muse_dtype of the tensor that the others go by."""
-    if t.dim() != 4 or t.dtype not in _CODE:
-        raise ValueError(f"{name}: expected float32 or bfloat16 with four dimensions, got {t.dtype} "
-                         f"{tuple(t.shape)}")
-    return t.shape, _CODE[t.dtype]
-
-
-def _call(fn: str, dev: int, *args):
-    """The call on the current stream of GPU `dev`, with that GPU current."""
-    f = getattr(_LIB or lib(), fn)
-    if torch._C._cuda_getDevice() == dev:
-        code = f(*args, torch._C._cuda_getCurrentRawStream(dev))
-    else:
-        with torch.cuda.device(dev):
-            code = f(*args, torch._C._cuda_getCurrentRawStream(dev))
-    if code:
-        _check(code, fn)
+def _serving():
+    global _SERVING
+    if _SERVING is None:
+        path = os.path.join(_HERE, "_serving.so")
+        if not os.path.exists(path):
+            raise RuntimeError(f"{path} is missing: build it with "
+                               "`python -m clustered_softmax_attention_b200.build`")
+        lib()
+        spec = importlib.util.spec_from_file_location("_serving", path)
+        mod = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(mod)
+        _SERVING = mod
+    return _SERVING
 
 
 def muse_rope_axes(Q, positions, sections, base: float = 10000.0, K=None, flags: int = 0,
@@ -482,43 +433,10 @@ def muse_rope_axes(Q, positions, sections, base: float = 10000.0, K=None, flags:
     int32 [B,axes,N] (or [axes,N], shared by the batch); sections: the pairs of each axis.
     Returns out, or (out, k_out) with K.  out may be Q itself, k_out K itself.  With
     MUSE_ROPE_INVERSE it turns back, which is the gradient."""
-    (B, H, N, D), code = _first(Q, "Q")
-    axes, dev = len(sections), Q.get_device()
-    if not 1 <= axes <= 4:
-        raise ValueError(f"sections: 1 to 4 axes, got {axes}")
-    nb = 1 if positions.dim() == 2 else B
-    pos = _ints(positions, (axes, N) if positions.dim() == 2 else (B, axes, N), "positions", dev)
-    if out is None:
-        out = Q.new_empty((B, H, N, D))
-    else:
-        _four(out, "out", Q.shape, Q)
-        _same_place(Q, out, "out")
-    k, ko, Hk = _NO_ROWS, _NO_ROWS, 0
-    if K is not None:
-        Hk = K.shape[1] if K.dim() == 4 else 0
-        _four(K, "K", (B, Hk, N, D), Q)
-        if k_out is None:
-            k_out = Q.new_empty((B, Hk, N, D))
-        else:
-            _four(k_out, "k_out", K.shape, Q)
-            _same_place(K, k_out, "k_out")
-        k, ko = _rows(K, "K"), _rows(k_out, "k_out", True)
-    _call("muse_rope_axes", dev, _rows(Q, "Q"), k, Hk, _dims7(B, H, N, D, D, code), pos, nb,
-          _rope(tuple(sections), float(base), flags), _rows(out, "out", True), ko)
-    return out if K is None else (out, k_out)
-
-
-_NO_ROWS = MuseRows()
-
-
-@functools.lru_cache(maxsize=64)
-def _rope(sections, base: float, flags: int) -> MuseRope:
-    return MuseRope(len(sections), (ctypes.c_int * 4)(*sections), base, flags)
-
-
-def _same_place(x: torch.Tensor, y: torch.Tensor, name: str):
-    if x.data_ptr() == y.data_ptr() and x.stride() != y.stride():
-        raise ValueError(f"{name}: in place needs the strides of its input")
+    r = (_SERVING or _serving()).rope_axes(Q, positions, sections, base, K, flags, out, k_out)
+    if r.__class__ is int:
+        _check(r, "muse_rope_axes")
+    return r
 
 
 def muse_cache_tile_bytes(D: int, Dv: int) -> int:
@@ -533,60 +451,30 @@ def muse_cache_shape(pages: int, Hkv: int, page: int, D: int, Dv: int):
     return pages, Hkv, page // 32, n
 
 
-def _cache(cache: torch.Tensor, page_table: torch.Tensor, B: int, D: int, dev: int):
-    """(muse_cache, Dv) of a cache tensor and its page table."""
-    if cache.dim() != 4 or cache.dtype != torch.uint8 or not cache.is_contiguous() \
-            or cache.get_device() != dev:
-        raise ValueError(f"cache: expected a contiguous uint8 tensor [pages,Hkv,page/32,bytes] on the "
-                         f"GPU of the other arguments, got {cache.dtype} {list(cache.shape)} on "
-                         f"{cache.device}")
-    if page_table.dim() != 2:
-        raise ValueError(f"page_table: expected [B,max_pages], got {list(page_table.shape)}")
-    pages, Hkv, tiles, size = cache.shape
-    Dv = size // 18 - D
-    if size % 18 or D not in (64, 128) or Dv not in (64, 128):
-        raise ValueError(f"cache: tiles of {size} bytes do not hold keys of width {D}")
-    slots = page_table.shape[1]
-    return MuseCache(cache.data_ptr(), _ints(page_table, (B, slots), "page_table", dev), pages, Hkv,
-                     tiles * 32, slots), Dv
-
-
 def muse_cache_write(cache, K, V, page_table, start, counts=None):
     """K [B,Hkv,N,D], V [B,Hkv,N,Dv] into the 4-bit cache as tokens start[b] + n, n < counts[b]
     (all N without counts).  Returns the cache."""
-    (B, H, N, D), code = _first(K, "K")
-    dev = K.get_device()
-    c, Dv = _cache(cache, page_table, B, D, dev)
-    if H != c.Hkv:
-        raise ValueError(f"K: shape {tuple(K.shape)}, the cache has {c.Hkv} heads")
-    _four(V, "V", (B, H, N, Dv), K)
-    _call("muse_cache_write", dev, _rows(K, "K"), _rows(V, "V"), _dims7(B, H, N, D, Dv, code), c,
-          _ints(start, (B,), "start", dev), _ints(counts, (B,), "counts", dev))
-    return cache
+    r = (_SERVING or _serving()).cache_write(cache, K, V, page_table, start, counts)
+    if r.__class__ is int:
+        _check(r, "muse_cache_write")
+    return r
 
 
 def muse_cache_read(cache, page_table, start, N: int, D: int, dtype=torch.bfloat16, counts=None,
                     out=None):
     """(K [B,Hkv,N,D], V [B,Hkv,N,Dv]) of tokens start[b] + n, n < counts[b]; rows from counts[b]
     on are left as they are (zero in tensors made here).  out: a (K, V) to read into."""
-    B, dev = page_table.shape[0], cache.get_device()
-    c, Dv = _cache(cache, page_table, B, D, dev)
     if out is None:
-        if dtype not in _CODE:
+        if dtype is not torch.bfloat16 and dtype is not torch.float32:
             raise ValueError(f"dtype: expected float32 or bfloat16, got {dtype}")
-        new = cache.new_empty if counts is None else cache.new_zeros
-        K, V = new((B, c.Hkv, N, D), dtype=dtype), new((B, c.Hkv, N, Dv), dtype=dtype)
+        K = V = None
     else:
         K, V = out
-        _first(K, "K")
-        if K.get_device() != dev:
-            raise ValueError(f"K: on {K.device}, the cache on {cache.device}")
-        _four(K, "K", (B, c.Hkv, N, D), K)
-        _four(V, "V", (B, c.Hkv, N, Dv), K)
-    _call("muse_cache_read", dev, _dims7(B, c.Hkv, N, D, Dv, _CODE[K.dtype]), c,
-          _ints(start, (B,), "start", dev), _ints(counts, (B,), "counts", dev),
-          _rows(K, "K", True), _rows(V, "V", True))
-    return K, V
+    r = (_SERVING or _serving()).cache_read(cache, page_table, start, N, D, dtype is torch.float32, counts,
+                                            K, V)
+    if r.__class__ is int:
+        _check(r, "muse_cache_read")
+    return r
 
 
 def muse_cache_attend(Q, cache, page_table, lens, counts=None, scale: float = 1.0,
@@ -596,25 +484,7 @@ def muse_cache_attend(Q, cache, page_table, lens, counts=None, scale: float = 1.
     token lens[b] - counts[b] + m (counts[b] = N without counts).  Returns (out [B,H,N,Dv],
     lse float32 [B,H,N]); rows from counts[b] on are left as they are (zero in tensors made
     here)."""
-    (B, H, N, D), code = _first(Q, "Q")
-    dev = Q.get_device()
-    c, Dv = _cache(cache, page_table, B, D, dev)
-    new = Q.new_empty if counts is None else Q.new_zeros
-    if out is None:
-        out = new((B, H, N, Dv))
-    else:
-        _four(out, "out", (B, H, N, Dv), Q)
-    if lse is None:
-        lse = new((B, H, N), dtype=torch.float32)
-    elif lse.shape != (B, H, N) or lse.dtype != torch.float32 or not lse.is_contiguous() \
-            or lse.get_device() != dev:
-        raise ValueError(f"lse: expected a contiguous float32 tensor {[B, H, N]} on {Q.device}")
-    d = _dims7(B, H, N, D, Dv, code, scale)
-    if ws is None:
-        ws = workspace("muse_cache_attend", d, c.Hkv, device=Q.device)
-    elif ws.dtype != torch.uint8 or not ws.is_contiguous() or ws.get_device() != dev:
-        raise ValueError(f"ws: expected a contiguous uint8 tensor on {Q.device}")
-    _call("muse_cache_attend", dev, _rows(Q, "Q"), d, c, _ints(lens, (B,), "lens", dev),
-          _ints(counts, (B,), "counts", dev), _rows(out, "out", True), lse.data_ptr(),
-          ws.data_ptr(), ws.numel())
-    return out, lse
+    r = (_SERVING or _serving()).cache_attend(Q, cache, page_table, lens, counts, scale, out, lse, ws)
+    if r.__class__ is int:
+        _check(r, "muse_cache_attend")
+    return r

@@ -143,26 +143,62 @@ def test_binding_refuses_what_the_library_cannot_see():
 
 
 def test_binding_refuses_overlapping_and_ragged_rows():
-    class Cuda:  # a tensor's geometry with is_cuda set: nothing here reaches the library
-        is_cuda, dtype = True, torch.bfloat16
+    """Geometry is refused before the device is looked at."""
+    table, start = torch.zeros(2, 2, dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
+    cache = torch.zeros(m.muse_cache_shape(4, 4, 64, 64, 64), dtype=torch.uint8)
+    buf = torch.zeros(1 << 16, dtype=torch.bfloat16)
+    view = lambda stride, at=0, shape=(2, 4, 8, 64): torch.as_strided(buf, shape, stride, at)
+    read = lambda k, v: m.muse_cache_read(cache, table, start, 8, 64, out=(k, v))
+    good = view((2048, 512, 64, 1))
+    for stride in ((2048, 512, 64, 2), (2048, 512, 68, 1)):
+        with pytest.raises(ValueError, match="16-byte"):
+            m.muse_cache_write(cache, view(stride), good, table, start)
+    with pytest.raises(ValueError, match="16-byte"):
+        m.muse_cache_write(cache, view((2048, 512, 64, 1), 1), good, table, start)
+    # rows that are read may repeat, or lie as [B,N,H,D]; they get as far as the device
+    for stride in ((0, 0, 64, 1), (2048, 64, 256, 1)):
+        with pytest.raises(ValueError, match="CUDA"):
+            m.muse_cache_write(cache, view(stride), good, table, start)
+    one = view((7, 64, 3, 1), shape=(1, 4, 1, 64))       # sizes of one have no stride
+    with pytest.raises(ValueError, match="CUDA"):
+        m.muse_cache_write(cache, one, one, table[:1], start[:1])
+    with pytest.raises(ValueError, match="CUDA"):
+        read(good, good)
 
-        def __init__(self, shape, stride, p=FAKE):
-            self.shape, self._s, self._p = shape, stride, p
 
-        def stride(self):
-            return self._s
+def test_binding_takes_nothing_but_what_it_names():
+    x = torch.zeros(2, 4, 8, 64, dtype=torch.bfloat16)
+    pos = torch.zeros(1, 8, dtype=torch.int32)
+    for bad in (None, 3, "x"):
+        with pytest.raises(ValueError, match="Q: expected a tensor"):
+            m.muse_rope_axes(bad, pos, [32])
+    with pytest.raises(ValueError, match="sections"):
+        m.muse_rope_axes(x, pos, [32.5])
+    with pytest.raises(TypeError, match="sections"):
+        m.muse_rope_axes(x, pos, 32)
+    with pytest.raises(ValueError, match="base"):
+        m.muse_rope_axes(x, pos, [32], base="a")
+    with pytest.raises(ValueError, match="sections"):
+        m.muse_rope_axes(x, pos, [2 ** 40])
+    with pytest.raises(ValueError, match="dtype"):
+        m.muse_cache_read(x, pos, pos, 8, 64, dtype=torch.float16)
+    with pytest.raises(TypeError, match="arguments"):
+        m._serving().rope_axes(x)
 
-        def data_ptr(self):
-            return self._p
 
-    ok = m._rows(Cuda((2, 4, 8, 64), (2048, 64, 256, 1)), "x", True)  # [B,N,H,D] memory
-    assert (ok.sb, ok.sh, ok.sn) == (2048, 64, 256)
-    one = m._rows(Cuda((1, 4, 1, 64), (7, 64, 3, 1)), "x", True)      # sizes of one have no stride
-    assert (one.sb, one.sn) == (0, 0)
-    m._rows(Cuda((2, 4, 8, 64), (0, 0, 64, 1)), "x")                  # a broadcast input
+@pytest.mark.gpu
+def test_binding_refuses_overlapping_rows_on_the_gpu():
+    pos = torch.zeros(1, 8, dtype=torch.int32, device="cuda")
+    buf = torch.zeros(1 << 16, dtype=torch.bfloat16, device="cuda")
+    x = buf[:4096].view(2, 4, 8, 64)
     for stride in ((0, 512, 64, 1), (2048, 512, 32, 1), (1024, 512, 64, 1)):
         with pytest.raises(ValueError, match="overlapping"):
-            m._rows(Cuda((2, 4, 8, 64), stride), "x", True)
-    for stride, p in (((2048, 512, 64, 2), FAKE), ((2048, 512, 68, 1), FAKE), ((2048, 512, 64, 1), FAKE + 2)):
-        with pytest.raises(ValueError, match="16-byte"):
-            m._rows(Cuda((2, 4, 8, 64), stride, p), "x")
+            m.muse_rope_axes(x, pos, [32], out=torch.as_strided(buf, (2, 4, 8, 64), stride, 8192))
+    with pytest.raises(ValueError, match="in place"):
+        m.muse_rope_axes(x, pos, [32], out=torch.as_strided(buf, (2, 4, 8, 64), (2048, 64, 256, 1)))
+    with pytest.raises(ValueError, match="positions"):
+        m.muse_rope_axes(x, pos.cpu(), [32])
+    with pytest.raises(m.MuseError, match="INVALID_ARG"):
+        m.muse_rope_axes(x, pos, [33])
+    with pytest.raises(m.MuseError, match="SHAPE"):
+        m.muse_rope_axes(x[..., :32].contiguous(), pos, [8])
