@@ -2,9 +2,10 @@
 //
 // A group of 32 neighbouring channels of one token has step = bf16(max|x| / 7) and codes
 // round_half_even(x / step), the code of the exact quotient:
-//   float32: t = rint(x * (1 / step)) is within one of it, r = x - t step is exact in float32
-//   (t step has at most 12 bits, and r is a multiple of the smaller of the two units and below
-//   x), and r against half a step, which is exact too, says whether t has to move;
+//   float32: t = x * (1 / step) rounded to a whole number (by adding 1.5 * 2^23) is within one
+//   of it, r = x - t step is exact in float32 (t step has at most 12 bits, and r is a multiple of
+//   the smaller of the two units and below x), and |r| against half a step, which is exact too,
+//   says whether t has to move: when above, or when equal and t is odd;
 //   bfloat16: x and step have 8 bits, so a quotient that is not half-way between two codes is at
 //   least 2^-10 from there.  x * (1 / step), off by 2^-20 at most, is rounded to a multiple of
 //   2^-14, which makes half-way quotients exact, and then to a whole number.
@@ -70,21 +71,32 @@ __device__ __forceinline__ uint16_t quantise(const float *p, uint32_t (&w)[Order
   uint16_t sb;
   const bool fine = group_step(top, step, sb);
   const bool tiny = !fine || step < 0x1p-100f;
-  const float inv = tiny ? 0.f : __frcp_rn(step), half = 0.5f * step;
+  if (tiny) {
+#pragma unroll
+    for (int k = 0; k < Order::kWords; ++k) {
+      w[k] = 0;
+#pragma unroll
+      for (int n = 0; n < Order::kNibbles; ++n)
+        w[k] |= (fine ? tiny_code(x[Order::channel(k, n)], step) : 8u) << (4 * n);
+    }
+    return sb;
+  }
+  const float inv = __frcp_rn(step), half = 0.5f * step;
 #pragma unroll
   for (int k = 0; k < Order::kWords; ++k) {
-    w[k] = 0;
+    uint32_t sum = 0, less = 0;
 #pragma unroll
     for (int n = 0; n < Order::kNibbles; ++n) {
       const float y = x[Order::channel(k, n)];
-      float t = rintf(y * inv);
-      const float r = fmaf(-t, step, y);
-      const bool odd = ((int)t & 1) != 0;
-      if (r > half || (r == half && odd)) t += 1.f;
-      else if (r < -half || (r == -half && odd)) t -= 1.f;
-      const uint32_t u = !fine ? 8u : tiny ? tiny_code(y, step) : (uint32_t)((int)t + 8);
-      w[k] |= u << (4 * n);
+      const float at = fmaf(y, inv, 12582912.f);  // its bits are 0x4B400000 + t
+      const float r = fmaf(12582912.f - at, step, y);
+      uint32_t t = __float_as_uint(at);
+      // the float below half a step when t is odd: then |r| = half moves too
+      if (fabsf(r) > __uint_as_float(__float_as_uint(half) - (t & 1u))) t += r > 0.f ? 1 : -1;
+      sum += t << (4 * n);
+      less += (0x4B400000u - 8u) << (4 * n);
     }
+    w[k] = sum - less;
   }
   return sb;
 }
@@ -200,18 +212,53 @@ __global__ void __launch_bounds__(D + Dv) cache_write(const CacheRows a, const C
   }
 }
 
+// Eight channels of a token: codes times the step, rounded once.
 __device__ __forceinline__ void store8(float *p, const float (&y)[8]) {
   reinterpret_cast<float4 *>(p)[0] = make_float4(y[0], y[1], y[2], y[3]);
   reinterpret_cast<float4 *>(p)[1] = make_float4(y[4], y[5], y[6], y[7]);
 }
-__device__ __forceinline__ void store8(__nv_bfloat16 *p, const float (&y)[8]) {
-  uint32_t w[4];
+// (x & 0x000f000f) | 0x43004300 in one operation: two codes as bfloat16 128 + u; less 136 they are
+// exact, and their product with the step is rounded once, as two values an operation.
+__device__ __forceinline__ uint32_t scaled_pair(uint32_t x, __nv_bfloat162 step) {
+  uint32_t y;
+  asm("lop3.b32 %0, %1, 0x000f000f, %2, 0xea;" : "=r"(y) : "r"(x), "r"(0x43004300u));
+  const __nv_bfloat162 less = __bfloat162bfloat162(__ushort_as_bfloat16(0xC308));  // -136
+  const __nv_bfloat162 v = __hmul2(__hadd2(*reinterpret_cast<__nv_bfloat162 *>(&y), less), step);
+  return *reinterpret_cast<const uint32_t *>(&v);
+}
+__device__ __forceinline__ void put_key(float *p, uint32_t w, uint16_t step) {
+  const float s = step_value(step);
+  float y[8];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 v = __floats2bfloat162_rn(y[2 * i], y[2 * i + 1]);
-    w[i] = *reinterpret_cast<const uint32_t *>(&v);
-  }
-  *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+  for (int n = 0; n < 8; ++n) y[n] = code_value(w, n) * s;
+  store8(p, y);
+}
+__device__ __forceinline__ void put_key(__nv_bfloat16 *p, uint32_t w, uint16_t step) {
+  const __nv_bfloat162 s = __bfloat162bfloat162(__ushort_as_bfloat16(step));
+  uint32_t c[4];  // channels n and n + 4
+#pragma unroll
+  for (int n = 0; n < 4; ++n) c[n] = scaled_pair(w >> (4 * n), s);
+  *reinterpret_cast<uint4 *>(p) =
+      make_uint4(__byte_perm(c[0], c[1], 0x5410), __byte_perm(c[2], c[3], 0x5410),
+                 __byte_perm(c[0], c[1], 0x7632), __byte_perm(c[2], c[3], 0x7632));
+}
+// w: the words of channel residues g = 0..7, of which nibble n is wanted.
+__device__ __forceinline__ void put_value(float *p, const uint32_t (&w)[8], int n, uint16_t step) {
+  const float s = step_value(step);
+  float y[8];
+#pragma unroll
+  for (int g = 0; g < 8; ++g) y[g] = code_value(w[g] >> (4 * n), 0) * s;
+  store8(p, y);
+}
+__device__ __forceinline__ void put_value(__nv_bfloat16 *p, const uint32_t (&w)[8], int n,
+                                          uint16_t step) {
+  const __nv_bfloat162 s = __bfloat162bfloat162(__ushort_as_bfloat16(step));
+  const uint32_t half = n & 4 ? 0x7632 : 0x5410;
+  uint32_t c[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    c[k] = scaled_pair(__byte_perm(w[2 * k], w[2 * k + 1], half) >> (4 * (n & 3)), s);
+  *reinterpret_cast<uint4 *>(p) = make_uint4(c[0], c[1], c[2], c[3]);
 }
 
 // One CTA per tile: the tile to shared memory, then eight channels of a token a thread, so
@@ -242,25 +289,38 @@ __global__ void __launch_bounds__(D + Dv) cache_read(const CacheRows a, const Ca
   const uint16_t *ks = reinterpret_cast<const uint16_t *>(img) + S::kKStep / 2;
   const uint16_t *vs = reinterpret_cast<const uint16_t *>(img) + S::kVStep / 2;
   const uint32_t *vw = img + S::kV / 4;
-  for (int i = tid; i < 32 * (D / 8); i += kThreads) {
-    const int t = i / (D / 8), j = i - t * (D / 8);
-    if (t < lo || t >= hi) continue;
-    const uint32_t w = img[key_word<D>(t, j & 3, j >> 2)];
-    const float step = step_value(ks[t * (D / 32) + (j >> 2)]);
-    float y[8];
+  T *kp = (T *)a.K.p + b * a.K.sb + h * a.K.sh + n0 * a.K.sn;
+  T *vp = (T *)a.V.p + b * a.V.sb + h * a.V.sh + n0 * a.V.sn;
 #pragma unroll
-    for (int n = 0; n < 8; ++n) y[n] = code_value(w, n) * step;
-    store8((T *)a.K.p + b * a.K.sb + h * a.K.sh + (n0 + t) * a.K.sn + 8 * j, y);
+  for (int i0 = 0; i0 < 32 * (D / 8); i0 += kThreads) {
+    const int i = i0 + tid;
+    if (32 * (D / 8) % kThreads && i >= 32 * (D / 8)) break;
+    const int t = i / (D / 8), j = i % (D / 8);
+    if (t >= lo && t < hi)
+      put_key(kp + t * a.K.sn + 8 * j, img[key_word<D>(t, j & 3, j >> 2)], ks[t * (D / 32) + (j >> 2)]);
   }
-  for (int i = tid; i < 32 * (Dv / 8); i += kThreads) {
-    const int t = i / (Dv / 8), j = i - t * (Dv / 8);
-    if (t < lo || t >= hi) continue;
-    const float step = step_value(vs[t * (Dv / 32) + (j >> 2)]);
-    float y[8];
+  // a thread takes nibble n of all words of a token: Dv / 64 runs of eight channels
 #pragma unroll
-    for (int g = 0; g < 8; ++g)
-      y[g] = code_value(vw[value_word<Dv>(t, g, j >> 3)] >> (4 * (j & 7)), 0) * step;
-    store8((T *)a.V.p + b * a.V.sb + h * a.V.sh + (n0 + t) * a.V.sn + 8 * j, y);
+  for (int i0 = 0; i0 < 32 * 8; i0 += kThreads) {
+    const int i = i0 + tid;
+    if (32 * 8 % kThreads && i >= 32 * 8) break;
+    const int t = i / 8, n = i % 8;
+    if (t < lo || t >= hi) continue;
+    uint32_t w[Dv / 64][8];
+#pragma unroll
+    for (int g = 0; g < 8; ++g) {
+      const uint32_t *at = vw + value_word<Dv>(t, g, 0);
+      if (Dv == 128) {
+        const uint2 x = *reinterpret_cast<const uint2 *>(at);
+        w[0][g] = x.x;
+        w[Dv / 64 - 1][g] = x.y;
+      } else {
+        w[0][g] = *at;
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < Dv / 64; ++k)
+      put_value(vp + t * a.V.sn + 64 * k + 8 * n, w[k], n, vs[t * (Dv / 32) + 2 * k + (n >> 2)]);
   }
 }
 
