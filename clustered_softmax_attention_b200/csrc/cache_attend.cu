@@ -19,144 +19,14 @@
 #include <algorithm>
 #include <atomic>
 
-#include <cuda_fp16.h>
-
-#include "cache.cuh"
+#include "cache_attend.cuh"
 
 namespace muse {
 namespace {
 
-constexpr int kMaxCtas = 592;   // 148 SMs x 4: the bound of the partials in the workspace
 constexpr int kWarps = 4;
 constexpr int kCluster = 8;      // CTAs of a cluster that takes an item
 constexpr int kClusterTiles = 16;  // of a token slice: the longest table that clusters take
-struct AttendArgs {
-  muse_rows Q, O;
-  float *lse;
-  const int32_t *lens, *counts;
-  int B, H, M, G;      // G = H / Hkv
-  int nrb;             // row blocks of an item's G * M rows
-  int min_tiles;       // a CTA takes at least so many
-  int cluster;         // CTAs of an item, or 0: stretches of the line
-  float scale;
-  float *part;         // [2 kMaxCtas][rows of a block][Dv]
-  float *part_ml;      // [2 kMaxCtas][rows of a block][2]
-  int2 *ends;          // [items]: slot of an item's first part, CTA of its last
-};
-
-// New rows, and tokens that the last of them may see, of sequence b.
-__device__ __forceinline__ int seq_rows(const AttendArgs &a, int b) {
-  if (!a.counts) return a.M;
-  return min(max(a.counts[b], 0), a.M);
-}
-__device__ __forceinline__ int seq_len(const AttendArgs &a, const CacheView &v, int b) {
-  const int64_t cap = (int64_t)v.max_pages << v.page_log2;
-  return (int)min((int64_t)max(a.lens[b], 0), cap);
-}
-// Lengths and counts outside their range: those tokens and rows are left out.
-__device__ __forceinline__ void check_lengths(const AttendArgs &a, const CacheView &v, int b,
-                                              int *status) {
-  if ((a.counts && seq_rows(a, b) != a.counts[b]) || seq_len(a, v, b) != a.lens[b])
-    report(status, MUSE_ERR_DEVICE);
-}
-__device__ __forceinline__ int seq_tiles(const AttendArgs &a, const CacheView &v, int b) {
-  return seq_rows(a, b) ? (seq_len(a, v, b) + kTile - 1) / kTile : 0;
-}
-
-// Beginning and ending an item (its queries, joining its sums) takes a CTA as long as kItemTiles
-// tiles: so many places on the line come before each item's tiles.  48 sequences of 0 to 8192
-// tokens, 8 heads: 182 us with 0, 93 with 6 and 10, 81 with 16; as many tokens in sequences of
-// one length: 79.
-constexpr int kItemTiles = 16;
-__device__ __forceinline__ int64_t seq_units(const AttendArgs &a, const CacheView &v, int b) {
-  const int nt = seq_tiles(a, v, b);
-  return nt ? (int64_t)(nt + kItemTiles) * v.Hkv * a.nrb : 0;
-}
-
-// The line of tiles: its length, and the sequence in which position x lies with the position
-// of that sequence's first tile.  Each thread sums a run of sequences.
-struct Line {
-  int64_t total, first;
-  int b;
-};
-template <int kThreads>
-__device__ __forceinline__ int64_t line_total(const AttendArgs &a, const CacheView &v, int64_t *run) {
-  const int tid = threadIdx.x, per = (a.B + kThreads - 1) / kThreads;
-  const int b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
-  int64_t s = 0;
-  for (int b = b0; b < b1; ++b) s += seq_units(a, v, b);
-  // inclusive scan over the threads
-  const int lane = tid & 31, warp = tid >> 5;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t y = __shfl_up_sync(0xffffffffu, s, o);
-    if (lane >= o) s += y;
-  }
-  if (lane == 31) run[kThreads + warp] = s;
-  __syncthreads();
-  int64_t add = 0;
-  for (int w = 0; w < warp; ++w) add += run[kThreads + w];
-  run[tid] = s + add;
-  __syncthreads();
-  return run[kThreads - 1];
-}
-template <int kThreads>
-__device__ __forceinline__ void line_find(const AttendArgs &a, const CacheView &v,
-                                          const int64_t *run, int64_t x, int &b, int64_t &first) {
-  int lo = 0, hi = kThreads - 1;  // the first thread whose run ends behind x
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (run[mid] > x) hi = mid;
-    else lo = mid + 1;
-  }
-  const int per = (a.B + kThreads - 1) / kThreads;
-  b = lo * per;
-  first = lo ? run[lo - 1] : 0;
-  while (b < a.B - 1) {
-    const int64_t n = seq_units(a, v, b);
-    if (first + n > x) break;
-    first += n;
-    ++b;
-  }
-}
-// A CTA's walk along the line, from x to x1, and the part of one item that it has come to.
-struct Walk {
-  int64_t x, x1, first;  // first: position of sequence b's first item
-  int b;
-};
-struct Span {
-  int b, hk, rb, t0, t1, nt, len, rows;
-  int parts_in;  // CTAs, from this one on, that the item's tiles lie in (where t0 is 0)
-};
-__device__ __noinline__ bool next_span(const AttendArgs &a, const CacheView &v, Walk &w, Span &s,
-                                       int64_t per) {
-  while (w.x < w.x1) {
-    int64_t units = seq_units(a, v, w.b);
-    while (w.x >= w.first + units) {
-      w.first += units;
-      units = seq_units(a, v, ++w.b);
-    }
-    const int nt = seq_tiles(a, v, w.b);
-    const int64_t in = w.x - w.first;
-    const uint32_t one = (uint32_t)(nt + kItemTiles);
-    const int item = in >> 32 ? (int)(in / one) : (int)((uint32_t)in / one);
-    const int64_t start = w.first + (int64_t)item * one + kItemTiles;  // of its tiles
-    s.b = w.b;
-    s.hk = item / a.nrb;
-    s.rb = item - s.hk * a.nrb;
-    s.nt = nt;
-    s.t0 = (int)max((int64_t)0, w.x - start);
-    s.t1 = (int)max((int64_t)0, min((int64_t)nt, w.x1 - start));
-    s.len = seq_len(a, v, w.b);
-    s.rows = seq_rows(a, w.b);
-    const int64_t left = w.x1 - start;  // tiles of the item up to this stretch's end
-    s.parts_in = left >= nt ? 1 : 1 + (int)((nt - left + per - 1) / per);
-    w.x = left >= nt ? start + nt : w.x1;
-    if (s.t0 < s.t1) return true;
-  }
-  return false;
-}
-
 // ------------------------------------------------------------------ small device pieces
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void *src) {
@@ -209,41 +79,6 @@ __device__ __forceinline__ uint32_t turned(uint32_t x) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
-__device__ __forceinline__ uint32_t bits(__half2 h) { return *reinterpret_cast<const uint32_t *>(&h); }
-__device__ __forceinline__ uint32_t bits(__nv_bfloat162 h) {
-  return *reinterpret_cast<const uint32_t *>(&h);
-}
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-  return bits(__floats2half2_rn(lo, hi));
-}
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-// (x & mask) | with in one operation (written out, it becomes two).
-template <uint32_t kMask>
-__device__ __forceinline__ uint32_t picked(uint32_t x, uint32_t with) {
-  uint32_t y;
-  asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(y) : "r"(x), "n"(kMask), "r"(with));
-  return y;
-}
-// Four pairs of codes of a word (nibbles n and n + 4) as float16: 1024 + u, or 1024 + 16 u,
-// without its offset.
-__device__ __forceinline__ void codes_f16(uint32_t x, uint32_t (&c)[4]) {
-  const uint32_t y = x >> 8;
-  const __half2 less = __half2half2(__ushort_as_half(0xE408));     // -1032
-  const __half2 part = __half2half2(__ushort_as_half(0x2C00));     // 1/16
-  const __half2 less16 = __half2half2(__ushort_as_half(0xD480));   // -72
-  constexpr uint32_t k1024 = 0x64006400u;
-  uint32_t t[4] = {picked<0x000f000fu>(x, k1024), picked<0x00f000f0u>(x, k1024),
-                   picked<0x000f000fu>(y, k1024), picked<0x00f000f0u>(y, k1024)};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __half2 h = *reinterpret_cast<const __half2 *>(&t[i]);
-    c[i] = bits(i & 1 ? __hfma2(h, part, less16) : __hadd2(h, less));
-  }
-}
 // The same pairs as bfloat16 (128 + u without its offset).
 __device__ __forceinline__ void codes_bf16(uint32_t x, uint32_t (&c)[4]) {
   const __nv_bfloat162 less = __bfloat162bfloat162(__ushort_as_bfloat16(0xC308));  // -136
@@ -253,8 +88,6 @@ __device__ __forceinline__ void codes_bf16(uint32_t x, uint32_t (&c)[4]) {
     c[i] = bits(__hadd2(*reinterpret_cast<const __nv_bfloat162 *>(&t), less));
   }
 }
-__device__ __forceinline__ float lo_f(uint32_t x) { return __uint_as_float(x << 16); }
-__device__ __forceinline__ float hi_f(uint32_t x) { return __uint_as_float(x & 0xffff0000u); }
 // Group w of two packed steps.
 template <int N>
 __device__ __forceinline__ float step_of(const uint32_t (&s)[N], int w) {
@@ -416,23 +249,6 @@ __device__ __forceinline__ void values_wide(Acc<Dv, NB> &acc, const uint8_t *cod
       for (int e = 0; e < 8; ++e)
         acc.o[nb][2 * grp + (e >> 2)][e & 3] += t[nb][e >> 2][e & 3];
   }
-}
-
-// Four channels of a row: sums y over weights of sum z at reference `at`.
-template <typename T>
-__device__ __forceinline__ void finish_row(const AttendArgs &a, int b, int h, int m, int c,
-                                           const float (&y)[4], float z, float at) {
-  const float inv = z == 0.f ? 0.f : 1.f / z;  // a row that sees nothing is zero
-  T *dst = (T *)a.O.p + b * a.O.sb + h * a.O.sh + m * a.O.sn + c;
-  if (sizeof(T) == 4) {
-    *reinterpret_cast<float4 *>(dst) = make_float4(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv);
-  } else {
-    *reinterpret_cast<uint2 *>(dst) = make_uint2(bits(__floats2bfloat162_rn(y[0] * inv, y[1] * inv)),
-                                                 bits(__floats2bfloat162_rn(y[2] * inv, y[3] * inv)));
-  }
-  if (c == 0 && a.lse)
-    a.lse[((int64_t)b * a.H + h) * a.M + m] =
-        z == 0.f ? -CUDART_INF_F : (at + log2f(z)) * 0.693147181f;
 }
 
 // One CTA: RT row tiles of 8 NB x kWarps / RT token slices.
@@ -917,80 +733,10 @@ attend(const __grid_constant__ AttendArgs a, const __grid_constant__ CacheView v
   cp_wait<0>();
 }
 
-// Rows of items that lie in several stretches (or in none: nothing to see).  One CTA per row: the
-// weights of all parts first, then their sums by four warps in turn, all loads independent, joined
-// in a fixed order.
-template <typename T, int Dv, int kRows>
-__global__ void __launch_bounds__(128) attend_join(const AttendArgs a, const CacheView v,
-                                                   int *status) {
-  constexpr int kThreads = 128, kGroups = kThreads / (Dv / 4);
-  __shared__ float s_w[kMaxCtas], s_red[8];
-  __shared__ float4 s_y[kGroups][Dv / 4];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int gr = blockIdx.x, hk = blockIdx.y, b = blockIdx.z;
-  dependents_may_launch();
-  wait_for_earlier();
-  const int rows = seq_rows(a, b);
-  if (gr == 0 && hk == 0 && tid == 0) check_lengths(a, v, b, status);
-  const int m = gr / a.G, h = hk * a.G + (gr - m * a.G);
-  const int nt = m < rows ? seq_tiles(a, v, b) : 0;
-  if (m >= rows) return;
-  const int rb = gr / kRows, row = gr - rb * kRows;
-  const int64_t item = ((int64_t)b * v.Hkv + hk) * a.nrb + rb;
-  const int2 ends = nt ? a.ends[item] : make_int2(0, -1);
-  const int c0 = ends.x >> 1, n = ends.y - c0 + 1;
-  if (n == 1) return;  // finished by its only CTA
-  // a part that begins its stretch is in the even slot: all but, perhaps, the first
-  auto slot_of = [&](int k) { return k ? 2 * (int64_t)(c0 + k) : (int64_t)ends.x; };
-  float ref = -CUDART_INF_F;
-  for (int k = tid; k < n; k += kThreads) {
-    const int64_t slot = slot_of(k);
-    s_w[k] = a.part_ml[(slot * kRows + row) * 2];
-    ref = fmaxf(ref, s_w[k]);
-  }
-  ref = warp_max(ref);
-  if (lane == 0) s_red[warp] = ref;
-  __syncthreads();
-  ref = fmaxf(fmaxf(s_red[0], s_red[1]), fmaxf(s_red[2], s_red[3]));
-  const float at = ref == -CUDART_INF_F ? 0.f : ref;
-  float z = 0.f;
-  for (int k = tid; k < n; k += kThreads) {
-    const int64_t slot = slot_of(k);
-    s_w[k] = ex2(s_w[k] - at);
-    z = fmaf(s_w[k], a.part_ml[(slot * kRows + row) * 2 + 1], z);
-  }
-  z = warp_sum(z);
-  if (lane == 0) s_red[4 + warp] = z;
-  __syncthreads();
-  z = (s_red[4] + s_red[5]) + (s_red[6] + s_red[7]);
-  const int grp = tid / (Dv / 4), c4 = tid - grp * (Dv / 4);
-  float y[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 8
-  for (int k = grp; k < n; k += kGroups) {
-    const int64_t slot = slot_of(k);
-    const float4 o = reinterpret_cast<const float4 *>(a.part + (slot * kRows + row) * Dv)[c4];
-    const float f = s_w[k];
-    y[0] = fmaf(f, o.x, y[0]);
-    y[1] = fmaf(f, o.y, y[1]);
-    y[2] = fmaf(f, o.z, y[2]);
-    y[3] = fmaf(f, o.w, y[3]);
-  }
-  s_y[grp][c4] = make_float4(y[0], y[1], y[2], y[3]);
-  __syncthreads();
-  if (grp) return;
-#pragma unroll
-  for (int k = 1; k < kGroups; ++k) {
-    const float4 o = s_y[k][c4];
-    y[0] += o.x;
-    y[1] += o.y;
-    y[2] += o.z;
-    y[3] += o.w;
-  }
-  finish_row<T>(a, b, h, m, 4 * c4, y, z, at);
+// Rows of a CTA: 8, 16, 32, 64 (float32: blocks of 64), or, in bfloat16, blocks of 128.
+int block_rows(int rows, int dtype) {
+  return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 || dtype == MUSE_F32 ? 64 : kTcRows;
 }
-
-// Rows of a CTA: 8, 16, 32 or blocks of 64 (a warp takes 8 or 16).
-int block_rows(int rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
 
 template <typename T, int D, int Dv, int NB, int RT>
 cudaError_t launch(AttendArgs a, const CacheView &v, int *status, cudaStream_t st) {
@@ -1016,6 +762,8 @@ cudaError_t launch(AttendArgs a, const CacheView &v, int *status, cudaStream_t s
   const int rows = a.G * a.M;
   a.nrb = (rows + C::kRows - 1) / C::kRows;
   a.min_tiles = C::kSlices;
+  a.tile_log2 = 5;
+  a.item_tiles = kItemTiles;
   const int64_t items = (int64_t)a.B * v.Hkv * a.nrb;
   const int64_t cap = ((int64_t)v.max_pages << v.page_log2) / kTile;  // tiles a sequence can have
   if (C::kClusters && cap <= kClusterTiles * C::kSlices && items * kCluster <= 2 * fit) {
@@ -1033,21 +781,23 @@ cudaError_t launch(AttendArgs a, const CacheView &v, int *status, cudaStream_t s
 
 template <typename T, int D, int Dv>
 cudaError_t by_rows(const AttendArgs &a, const CacheView &v, int *status, cudaStream_t st) {
-  switch (block_rows(a.G * a.M)) {
+  switch (block_rows(a.G * a.M, sizeof(T) == 4 ? MUSE_F32 : MUSE_BF16)) {
     case 8: return launch<T, D, Dv, 1, 1>(a, v, status, st);
     case 16: return launch<T, D, Dv, 2, 1>(a, v, status, st);
     case 32: return launch<T, D, Dv, 2, 2>(a, v, status, st);
-    default: return launch<T, D, Dv, 2, 4>(a, v, status, st);
+    case 64: return launch<T, D, Dv, 2, 4>(a, v, status, st);
+    default: return launch_attend_tc<D, Dv>(a, v, status, st);
   }
 }
 
 // Partial sums and references of two parts a CTA, and the ends of every item.
 struct AttendWs {
   size_t part, part_ml, ends;
-  AttendWs(int64_t B, int64_t H, int64_t M, int64_t Dv, int64_t Hkv) {
-    const int64_t all = H / Hkv * M, rows = block_rows((int)std::min<int64_t>(all, 1 << 20));
-    part = align_up((size_t)(2 * kMaxCtas * rows * Dv * 4));
-    part_ml = align_up((size_t)(2 * kMaxCtas * rows * 8));
+  AttendWs(int64_t B, int64_t H, int64_t M, int64_t Dv, int64_t Hkv, int dtype) {
+    const int64_t all = H / Hkv * M, rows = block_rows((int)std::min<int64_t>(all, 1 << 20), dtype);
+    const int64_t slots = 2 * (rows == kTcRows ? kTcMaxCtas : kMaxCtas);
+    part = align_up((size_t)(slots * rows * Dv * 4));
+    part_ml = align_up((size_t)(slots * rows * 8));
     ends = align_up((size_t)(B * Hkv * ((all + rows - 1) / rows) * 8));
   }
 };
@@ -1063,7 +813,7 @@ cudaError_t by_width(const AttendArgs &a, const muse_dims &d, const CacheView &v
 }  // namespace
 
 size_t cache_attend_ws(const muse_dims &d, int Hkv) {
-  const AttendWs w(d.B, d.H, d.N, d.Dv, Hkv);
+  const AttendWs w(d.B, d.H, d.N, d.Dv, Hkv, d.dtype);
   return w.part + w.part_ml + w.ends;
 }
 
@@ -1080,9 +830,9 @@ cudaError_t run_cache_attend(const muse_rows &Q, const muse_dims &d, const muse_
   a.H = d.H;
   a.M = d.N;
   a.G = d.H / c.Hkv;
-  a.nrb = a.min_tiles = a.cluster = 0;
+  a.nrb = a.min_tiles = a.tile_log2 = a.item_tiles = a.cluster = 0;
   a.scale = d.scale;
-  const AttendWs w(d.B, d.H, d.N, d.Dv, c.Hkv);
+  const AttendWs w(d.B, d.H, d.N, d.Dv, c.Hkv, d.dtype);
   char *p = static_cast<char *>(ws);
   a.part = reinterpret_cast<float *>(p);
   a.part_ml = reinterpret_cast<float *>(p + w.part);

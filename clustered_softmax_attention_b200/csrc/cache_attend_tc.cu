@@ -1,0 +1,646 @@
+// Causal attention over the 4-bit cache for many rows of a cache head (the chunk of a prompt, many
+// drafted tokens): more than 64 bfloat16 rows, 128 at a time, on tcgen05.
+//
+// With that many rows the products bound it, not the cache's bytes, and a code is dequantised once
+// for 128 rows into shared memory instead of into every warp's registers.  Per tile of 128 tokens:
+//   producers (8 warps)  codes -> float16 K' and V' in 128-byte swizzled shared memory, two stages;
+//   issuer               S = Q K'^T into TMEM (two buffers), O += P V' with P from TMEM;
+//   softmax (4 warps)    a row a thread: S from TMEM, weights to TMEM, O in TMEM moved only
+//                        when the running reference moves.
+// S of the next tile is issued before O += P V' of this one, so the softmax of one tile runs
+// beside both products.
+//   K' = code step 2^(12 - e), e the exponent of the token's largest step: exact while the token's
+//   groups are within 2^26 of each other; 2^(e - 12) multiplies the token's column of S.
+//   V' = code step unit[group], a power of two that the span's first tile sets; exact for steps
+//   from 2^-10 to 2^5 of its largest, and, zero steps apart, a tile with others makes the span go
+//   the slow way: its rows are computed again in float32 from the codes.
+// The order of channels inside K' and V' is the one in which a word's codes come out, two nibbles
+// four apart a register; Q is laid out alike, and the output's columns are put back at the end.
+#include "cache_attend.cuh"
+#include "tc_ptx.cuh"
+
+namespace muse {
+namespace {
+
+using namespace ptx;
+
+constexpr int kTok = 128;               // tokens of a tile
+constexpr int kSoftmaxWarps = 4, kProducers = 8, kIssuer = kSoftmaxWarps + kProducers;
+constexpr int kThreads = 32 * (kIssuer + 1);
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kS = 0, kO = 256, kP = 384;  // TMEM columns: S (two of 128), O, P (two of 64)
+
+template <int D, int Dv>
+struct __align__(1024) Smem {
+  __half q[D / 64][kTcRows * 64];
+  __half k[2][D / 64][kTok * 64];
+  __half v[2][Dv / 64][kTok * 64];
+  // a producer's sixteen tokens as they are held: key codes, value codes, key steps, value steps
+  uint8_t raw[kProducers][2][9 * (D + Dv)];
+  float tokf[2][kTok];        // what a token's column of S is multiplied by
+  float unit[4][Dv / 32];     // by span
+  uint32_t big[2][kProducers][Dv / 64];  // by span
+  float slow_q[kSoftmaxWarps][D];
+  int bad[4];                 // number (from 1) of the last span that has to go the slow way
+  int gone[2][kProducers];    // sixteen tokens that are not in the cache
+  int64_t run[kThreads + kThreads / 32];
+  uint64_t q_full, unit_full, kv_full[2], kv_empty[2], s_full[2], p_full[2], end;
+  uint32_t tmem_base;
+  int abort_flag;
+};
+
+// Instruction descriptor: float16 operands, float32 accumulators.
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N) {
+  return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+// MN-major operand, 128-byte swizzle: 64 channels of a token a row, blocks of 64 channels 16 KB
+// apart.
+__device__ __forceinline__ uint64_t sdesc_mn(const void *p) {
+  const uint32_t a = saddr(p);
+  uint64_t d = 0;
+  d |= (uint64_t)((a & 0x3FFFFu) >> 4);
+  d |= (uint64_t)((16384u >> 4) & 0x3FFFu) << 16;
+  d |= (uint64_t)(1024 >> 4) << 32;
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)2 << 61;
+  return d;
+}
+__device__ __forceinline__ void async_fence() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+// Waits for this thread's TMEM loads; x, the last of them, is not used before.
+__device__ __forceinline__ void arrived(uint32_t (&x)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(x[0]), "+r"(x[1]), "+r"(x[2]), "+r"(x[3]), "+r"(x[4]), "+r"(x[5]), "+r"(x[6]),
+                 "+r"(x[7]), "+r"(x[8]), "+r"(x[9]), "+r"(x[10]), "+r"(x[11]), "+r"(x[12]),
+                 "+r"(x[13]), "+r"(x[14]), "+r"(x[15])
+               :
+               : "memory");
+}
+// The 16-byte chunk c of a 128-byte row.
+__device__ __forceinline__ uint4 *chunk(__half *block, int row, int c) {
+  return reinterpret_cast<uint4 *>(reinterpret_cast<char *>(block) + row * 128 + ((c ^ (row & 7)) << 4));
+}
+// Column of O (within 64) that holds channel c of 64.
+__host__ __device__ constexpr int column_of(int c) {
+  return 8 * (c % 8) + (c / 8 < 4 ? 2 * (c / 8) : 2 * (c / 8 - 4) + 1);
+}
+
+// One row over the 32-token tiles [lo, hi) of its item, in float32 from the codes: a lane a token
+// for the logits, a channel of every group for the values.
+template <int D, int Dv>
+__device__ __noinline__ void slow_row(const AttendArgs &a, const CacheView &v, int b, int hk, int see,
+                                      int lo, int hi, const float *q, float &mx, float &l,
+                                      float (&o)[Dv / 32]) {
+  using S = TileShape<D, Dv>;
+  const int lane = threadIdx.x & 31;
+  mx = -CUDART_INF_F;
+  l = 0.f;
+  for (int g = 0; g < Dv / 32; ++g) o[g] = 0.f;
+  for (int tile = lo; tile < hi && tile * 32 < see; ++tile) {
+    const uint8_t *p = cache_tile(v, b, hk, tile, S::kBytes);
+    if (!p) continue;
+    const uint32_t *kw = (const uint32_t *)p, *vw = (const uint32_t *)(p + S::kV);
+    const uint16_t *ks = (const uint16_t *)(p + S::kKStep), *vs = (const uint16_t *)(p + S::kVStep);
+    float x = 0.f;
+    for (int w = 0; w < D / 32; ++w) {
+      float s = 0.f;
+      for (int c = 0; c < 4; ++c) {
+        const uint32_t u = kw[key_word<D>(lane, c, w)];
+        for (int n = 0; n < 8; ++n) s = fmaf(code_value(u, n), q[32 * w + 8 * c + n], s);
+      }
+      x = fmaf(s, step_value(ks[lane * (D / 32) + w]), x);
+    }
+    const bool live = tile * 32 + lane < see;
+    const float top = fmaxf(mx, warp_max(live ? x : -CUDART_INF_F));
+    const float ref = top == -CUDART_INF_F ? 0.f : top;
+    const float fix = ex2(mx - ref), e = live ? ex2(x - ref) : 0.f;
+    mx = top;
+    l = l * fix + warp_sum(e);
+    for (int g = 0; g < Dv / 32; ++g) o[g] *= fix;
+    const int n = min(32, see - tile * 32);
+    for (int t = 0; t < n; ++t) {
+      const float pt = __shfl_sync(0xffffffffu, e, t);
+      for (int g = 0; g < Dv / 32; ++g) {
+        const int c = 32 * g + lane;
+        const uint32_t u = vw[value_word<Dv>(t, c & 7, c >> 6)] >> (4 * ((c & 63) >> 3));
+        o[g] = fmaf(pt * step_value(vs[t * (Dv / 32) + g]), code_value(u, 0), o[g]);
+      }
+    }
+  }
+}
+
+template <int D, int Dv>
+__global__ void __launch_bounds__(kThreads, 1)
+attend_tc(const __grid_constant__ AttendArgs a, const __grid_constant__ CacheView v, int *status) {
+  using S = TileShape<D, Dv>;
+  constexpr int NGk = D / 32, NG = Dv / 32;
+  constexpr unsigned kAll = 0xffffffffu;
+  extern __shared__ unsigned char smem_raw[];
+  Smem<D, Dv> &sm = *reinterpret_cast<Smem<D, Dv> *>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q = lane & 3;
+  volatile int *abort_flag = &sm.abort_flag;
+  dependents_may_launch();
+  wait_for_earlier();
+
+  const int64_t total = line_total<kThreads>(a, v, sm.run);
+  const int64_t per = max((int64_t)a.min_tiles, (total + gridDim.x - 1) / gridDim.x);
+  Walk walk;
+  Span sp;
+  walk.x = blockIdx.x * per;
+  walk.x1 = min(total, walk.x + per);
+  if (walk.x >= walk.x1) return;
+  line_find<kThreads>(a, v, sm.run, walk.x, walk.b, walk.first);
+  if (!next_span(a, v, walk, sp, per)) return;
+
+  if (tid == 0) {
+    mbar_init(&sm.q_full, 128);
+    mbar_init(&sm.unit_full, 32 * kProducers);
+    mbar_init(&sm.end, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sm.kv_full[i], 32 * kProducers);
+      mbar_init(&sm.kv_empty[i], 1);
+      mbar_init(&sm.s_full[i], 1);
+      mbar_init(&sm.p_full[i], 128);
+    }
+    for (int i = 0; i < 4; ++i) sm.bad[i] = 0;
+    sm.abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 0) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     saddr(&sm.tmem_base)),
+                 "r"(kTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem_base;
+
+  uint32_t it = 0;  // tiles so far, in every role alike
+  // a wait that gives up ends the warp's role; the others end at their own next wait
+  bool ok = true;
+  auto wait = [&](uint64_t *bar, uint32_t phase) {
+    ok = __all_sync(kAll, mbar_wait(bar, phase & 1, abort_flag, status));
+    return ok;
+  };
+
+  if (warp >= kSoftmaxWarps && warp < kIssuer) {
+    // ------------------------------------------------------------ codes -> float16 operands
+    const int pw = warp - kSoftmaxWarps;  // tokens 16 pw .. 16 pw + 15 of a tile
+    constexpr int kRV = 8 * D, kRKS = 8 * (D + Dv), kRVS = kRKS + D;
+    uint32_t shift[Dv / 64];
+    // the tile after the one at hand is under way: raw[it & 1] holds tile it
+    bool next_here = false;
+    auto fetch = [&](const Span &s, int t, uint32_t slot) {
+      const int tile = 4 * t + (pw >> 1), part = pw & 1;
+      const uint8_t *p = nullptr;
+      if (tile * 32 + 16 * part < s.len) {
+        p = cache_tile(v, s.b, s.hk, tile, S::kBytes);
+        if (!p && lane == 0) report(status, MUSE_ERR_DEVICE);
+      }
+      if (p) {
+        uint8_t *to = sm.raw[pw][slot & 1];
+#pragma unroll
+        for (int i = 0; i < D / 2; i += 32)
+          cp_async16(to + (i + lane) * 16, p + S::kK + part * 8 * D + (i + lane) * 16, 16);
+#pragma unroll
+        for (int i = 0; i < Dv / 2; i += 32)
+          cp_async16(to + kRV + (i + lane) * 16, p + S::kV + part * 8 * Dv + (i + lane) * 16, 16);
+        if (lane < D / 16) cp_async16(to + kRKS + lane * 16, p + S::kKStep + part * D + lane * 16, 16);
+        else if (lane >= 16 && lane < 16 + Dv / 16)
+          cp_async16(to + kRVS + (lane - 16) * 16, p + S::kVStep + part * Dv + (lane - 16) * 16, 16);
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+      next_here = p != nullptr;
+    };
+    fetch(sp, sp.t0, 0);
+    bool more = true;
+    for (int span = 1; more && ok; ++span) {
+      const Span cur = sp;
+      more = next_span(a, v, walk, sp, per);
+      for (int t = cur.t0; t < cur.t1 && ok; ++t, ++it) {
+        const uint32_t st = it & 1;
+        const int base = t * kTok + pw * 16;
+        const bool here = next_here;
+        if (t + 1 < cur.t1) fetch(cur, t + 1, it + 1);
+        else if (more) fetch(sp, sp.t0, it + 1);
+        else asm volatile("cp.async.commit_group;" ::: "memory");
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+        __syncwarp();
+        const uint8_t *raw = sm.raw[pw][st];
+        const int n = here ? min(16, cur.len - base) : 0;  // its tokens
+        if (t == cur.t0) {
+          // the values' unit: the span's first tile's largest step comes to [2^3, 2^4)
+          uint32_t big[Dv / 64];
+#pragma unroll
+          for (int w = 0; w < Dv / 64; ++w) {
+            // a lane a token; NaN is negative here, and left out
+            big[w] = lane < n ? __vmaxs2(0u, reinterpret_cast<const uint32_t *>(raw + kRVS)[lane * (Dv / 64) + w]) : 0u;
+#pragma unroll
+            for (int o = 16; o; o >>= 1) big[w] = __vmaxs2(big[w], __shfl_xor_sync(kAll, big[w], o));
+            if (lane == 0) sm.big[span & 1][pw][w] = big[w];
+          }
+          mbar_arrive(&sm.unit_full);
+          if (!wait(&sm.unit_full, span - 1)) break;
+#pragma unroll
+          for (int w = 0; w < Dv / 64; ++w) {
+#pragma unroll
+            for (int k = 0; k < kProducers; ++k) big[w] = __vmaxs2(big[w], sm.big[span & 1][k][w]);
+            shift[w] = 0;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const int ex = min(max((int)((big[w] >> (16 * k + 7)) & 255u) - 127, -40), 60);
+              // float16's exponent is 112 less than bfloat16's
+              shift[w] += (uint32_t)((3 - ex - 112) * 128) << (16 * k);
+              if (pw == 0 && lane == 0) sm.unit[span & 3][2 * w + k] = ldexpf(1.f, 3 - ex);
+            }
+          }
+        }
+        if (it >= 2 && !wait(&sm.kv_empty[st], (it - 2) >> 1)) break;
+        if (lane == 0) sm.gone[st][pw] = !here && base < cur.len;
+        // (loops, not unrolled: one warp a scheduler runs this, and straight code of its length
+        // would wait for its instructions)
+#pragma unroll 1
+        for (int i = 0; i < 2; ++i) {
+          // ---- keys: row 8 i + g, a chunk of eight channels a word
+          {
+            const int row = pw * 16 + 8 * i + g;
+            const bool live = 8 * i + g < n;
+            uint32_t kw[NGk], ks[NGk / 2], top = 0;
+            if (D == 128) {
+              const uint4 x = reinterpret_cast<const uint4 *>(raw)[i * 32 + lane];
+              const uint2 y = reinterpret_cast<const uint2 *>(raw + kRKS)[8 * i + g];
+              kw[0] = x.x;
+              kw[1] = x.y;
+              kw[NGk - 2] = x.z;
+              kw[NGk - 1] = x.w;
+              ks[0] = y.x;
+              ks[NGk / 2 - 1] = y.y;
+            } else {
+              const uint2 x = reinterpret_cast<const uint2 *>(raw)[lane * 2 + i];
+              kw[0] = x.x;
+              kw[1] = x.y;
+              ks[0] = reinterpret_cast<const uint32_t *>(raw + kRKS)[8 * i + g];
+            }
+            bool nan = false;
+#pragma unroll
+            for (int w = 0; w < NGk / 2; ++w) {
+              if (!live) ks[w] = 0;
+              nan |= (ks[w] & 0x80008000u) != 0;
+              top = __vmaxu2(top, ks[w]);
+            }
+            const int e = (int)(max(top & 0xffffu, top >> 16) >> 7);
+            if (q == 0) sm.tokf[st][row] = !live ? 0.f : nan ? CUDART_NAN_F : ldexpf(1.f, e - 127 - 12);
+#pragma unroll
+            for (int w = 0; w < NGk; ++w) {
+              const int s = (int)((ks[w >> 1] >> (16 * (w & 1))) & 0xffffu);
+              const int f = s - (e - 27) * 128;  // exponent field at most 27
+              const bool keep = !nan && s >= 128 && f >= 128;
+              const __half2 step = __half2half2(__ushort_as_half(keep ? (unsigned short)(f << 3) : 0));
+              uint32_t c[4];
+              codes_f16(kw[w], c);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) c[k] = bits(__hmul2(*reinterpret_cast<__half2 *>(&c[k]), step));
+              *chunk(sm.k[st][w >> 1], row, (w & 1) * 4 + q) = make_uint4(c[0], c[1], c[2], c[3]);
+            }
+          }
+          // ---- values: rows 8 i + 2 q and + 1, chunk g: the word's eight channels
+          uint32_t vw[2][Dv / 64], vs[2][Dv / 64], off_range = 0;
+          if (Dv == 128) {
+            const uint4 x = reinterpret_cast<const uint4 *>(raw + kRV)[i * 32 + lane];
+            const uint4 y = reinterpret_cast<const uint4 *>(raw + kRVS)[4 * i + q];
+            vw[0][0] = x.x;
+            vw[0][Dv / 64 - 1] = x.y;
+            vw[1][0] = x.z;
+            vw[1][Dv / 64 - 1] = x.w;
+            vs[0][0] = y.x;
+            vs[0][Dv / 64 - 1] = y.y;
+            vs[1][0] = y.z;
+            vs[1][Dv / 64 - 1] = y.w;
+          } else {
+            const uint2 x = reinterpret_cast<const uint2 *>(raw + kRV)[lane * 2 + i];
+            const uint2 y = reinterpret_cast<const uint2 *>(raw + kRVS)[4 * i + q];
+            vw[0][0] = x.x;
+            vw[1][0] = x.y;
+            vs[0][0] = y.x;
+            vs[1][0] = y.y;
+          }
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int w = 0; w < Dv / 64; ++w)  // exponent fields 8..23, 18 the first tile's largest
+              if (8 * i + 2 * q + e < n) off_range |= vs[e][w] + shift[w] - 0x04000400u;
+          const bool odd = __any_sync(kAll, off_range & 0xf800f800u);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int row = pw * 16 + 8 * i + 2 * q + e;
+            const bool live = 8 * i + 2 * q + e < n;
+#pragma unroll
+            for (int w = 0; w < Dv / 64; ++w) {
+              uint32_t d = (vs[e][w] + shift[w]) << 3;
+              if (__builtin_expect(odd, 0)) {
+                // half by half: a zero step is zero; a float16 from 2^-14 on will do; else slow
+                d = 0;
+                const int low = (short)(shift[w] & 0xffffu), high = (short)((shift[w] - (uint32_t)low) >> 16);
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                  const int s = (int)((vs[e][w] >> (16 * k)) & 0xffffu), f = s + (k ? high : low);
+                  if (!live || s == 0) continue;
+                  if (s >= 0x7f80 || f < 128 || f >= 28 * 128) sm.bad[span & 3] = span;
+                  else d |= (uint32_t)(f << 3) << (16 * k);
+                }
+              }
+              if (!live) d = 0;
+              uint32_t c[4];
+              codes_f16(vw[e][w], c);
+              const __half2 step = *reinterpret_cast<__half2 *>(&d);  // nibbles 0..3, 4..7
+#pragma unroll
+              for (int k = 0; k < 4; ++k) c[k] = bits(__hmul2(*reinterpret_cast<__half2 *>(&c[k]), step));
+              *chunk(sm.v[st][w], row, g) = make_uint4(c[0], c[1], c[2], c[3]);
+            }
+          }
+        }
+        async_fence();
+        mbar_arrive(&sm.kv_full[st]);
+      }
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+  } else if (warp == kIssuer) {
+    // ------------------------------------------------------------ products
+    bool more = true;
+    for (int span = 1; more && ok; ++span) {
+      const int n = sp.t1 - sp.t0;
+      more = next_span(a, v, walk, sp, per);
+      const uint32_t it0 = it;
+      if (!wait(&sm.q_full, span - 1)) break;
+      auto values = [&](uint32_t u) {  // O += P V' of tile u
+        if (!wait(&sm.p_full[u & 1], u >> 1)) return;
+        tc_fence_after();
+        if (lane == 0) {
+          constexpr uint32_t id = idesc_f16(kTcRows, Dv) | (1u << 16);
+          for (int kk = 0; kk < kTok / 16; ++kk)
+            tc_mma_ts(tmem + kO, tmem + kP + (u & 1) * 64 + kk * 8, sdesc_mn(sm.v[u & 1][0] + kk * 16 * 64),
+                      id, u > it0 || kk > 0 ? 1u : 0u);
+          tc_commit(&sm.kv_empty[u & 1]);
+        }
+        __syncwarp();
+      };
+      for (int i = 0; i < n && ok; ++i, ++it) {
+        if (!wait(&sm.kv_full[it & 1], it >> 1)) break;
+        tc_fence_after();
+        if (lane == 0) {
+          constexpr uint32_t id = idesc_f16(kTcRows, kTok);
+          for (int kk = 0; kk < D / 16; ++kk)
+            tc_mma(tmem + kS + (it & 1) * 128, sdesc(sm.q[kk / 4] + (kk % 4) * 16),
+                   sdesc(sm.k[it & 1][kk / 4] + (kk % 4) * 16), id, kk > 0 ? 1u : 0u);
+          tc_commit(&sm.s_full[it & 1]);
+        }
+        __syncwarp();
+        if (i) values(it - 1);
+      }
+      if (ok) values(it - 1);
+    }
+  } else {
+    // ------------------------------------------------------------ softmax: row tid
+    const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
+    bool more = true;
+    for (int span = 1; more && ok; ++span) {
+      const Span cur = sp;
+      more = next_span(a, v, walk, sp, per);
+      const int gr = cur.rb * kTcRows + tid;
+      const int m = gr / a.G, h = cur.hk * a.G + (gr - m * a.G);
+      const bool live = m < cur.rows;
+      const int see = live ? min(max(cur.len - cur.rows + m + 1, 0), cur.len) : 0;
+      int see_all = see;
+#pragma unroll
+      for (int x = 16; x; x >>= 1) see_all = min(see_all, __shfl_xor_sync(kAll, see_all, x));
+      // ---- the query as float16, a power of two a row: its largest in [2^14, 2^15)
+      float rf;
+      {
+        const uint4 *from = reinterpret_cast<const uint4 *>(
+            (const __nv_bfloat16 *)a.Q.p + cur.b * a.Q.sb + h * a.Q.sh + m * a.Q.sn);
+        uint32_t top = 0;
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+          const uint4 x = live ? from[i] : make_uint4(0, 0, 0, 0);
+          top = __vmaxu2(__vmaxu2(top, x.x & 0x7fff7fffu), x.y & 0x7fff7fffu);
+          top = __vmaxu2(__vmaxu2(top, x.z & 0x7fff7fffu), x.w & 0x7fff7fffu);
+        }
+        top = max(top << 16, top & 0xffff0000u);
+        const int e = min(max((int)(top >> 23) - 127 - 14, -114), 113);
+        const float mul = top >= 0x7f800000u ? CUDART_NAN_F : a.scale < 0.f ? -ldexpf(1.f, -e) : ldexpf(1.f, -e);
+        rf = fmaxf(ldexpf(fabsf(a.scale) * 1.44269504f, e), 1e-37f);
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+          const uint4 x = live ? from[i] : make_uint4(0, 0, 0, 0);
+          // channels (0, 4), (1, 5), (2, 6), (3, 7) of eight
+          *chunk(sm.q[i / 8], tid, i % 8) =
+              make_uint4(pack_f16(lo_f(x.x) * mul, lo_f(x.z) * mul), pack_f16(hi_f(x.x) * mul, hi_f(x.z) * mul),
+                         pack_f16(lo_f(x.y) * mul, lo_f(x.w) * mul), pack_f16(hi_f(x.y) * mul, hi_f(x.w) * mul));
+        }
+      }
+      async_fence();
+      mbar_arrive(&sm.q_full);
+
+      float mx = -CUDART_INF_F, l = 0.f;
+      const uint32_t it0 = it;
+      for (int t = cur.t0; t < cur.t1 && ok; ++t, ++it) {
+        const uint32_t st = it & 1, col = tmem + lane_base + kS + st * 128;
+        if (!wait(&sm.kv_full[st], it >> 1) || !wait(&sm.s_full[st], it >> 1)) break;
+        tc_fence_after();
+        const float4 *tf = reinterpret_cast<const float4 *>(sm.tokf[st]);
+        const int left = see - t * kTok;
+        int gone = 0;
+#pragma unroll
+        for (int k = 0; k < kProducers; ++k) gone |= sm.gone[st][k] << k;
+        const bool edge = see_all - t * kTok < kTok || gone;
+        // weights are 2^9 at the reference, which moves when one would pass 2^14: they are formed
+        // with the reference as it is, and, where it has to move (the first tile, a few more),
+        // once again
+        float sum;
+        for (int again = 0;; ++again) {
+          float top = -CUDART_INF_F;
+          sum = 0.f;
+          const float ref = mx == -CUDART_INF_F ? 0.f : mx;
+          uint32_t x[2][16];
+          tmem_ld16_async(col, x[0]);
+#pragma unroll 1
+          for (int c = 0; c < 8; c += 2) {
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              arrived(x[k]);
+              if (c + k < 7) tmem_ld16_async(col + (c + k + 1) * 16, x[k ^ 1]);
+              float y[16];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float4 f = tf[4 * (c + k) + e];
+                y[4 * e] = __uint_as_float(x[k][4 * e]) * f.x;
+                y[4 * e + 1] = __uint_as_float(x[k][4 * e + 1]) * f.y;
+                y[4 * e + 2] = __uint_as_float(x[k][4 * e + 2]) * f.z;
+                y[4 * e + 3] = __uint_as_float(x[k][4 * e + 3]) * f.w;
+              }
+              if (__builtin_expect(edge, 0)) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                  if (16 * (c + k) + e >= left || (gone >> (c + k)) & 1) y[e] = -CUDART_INF_F;
+              }
+              uint32_t pk[8];
+#pragma unroll
+              for (int e = 0; e < 16; e += 2) {
+                top = fmaxf(top, fmaxf(y[e], y[e + 1]));
+                const float p0 = ex2(fmaf(y[e], rf, -ref)), p1 = ex2(fmaf(y[e + 1], rf, -ref));
+                sum += p0 + p1;
+                pk[e >> 1] = pack_f16(p0, p1);
+              }
+              tmem_st8(tmem + lane_base + kP + st * 64 + (c + k) * 8, pk);
+            }
+          }
+          tmem_st_wait();
+          if (again || __builtin_expect(!__any_sync(kAll, top * rf > mx + 14.f), 1)) break;
+          const float now = fmaxf(mx, top * rf - 9.f);
+          const float fix = now == -CUDART_INF_F ? 1.f : ex2(mx - now);
+          mx = now;
+          l *= fix;
+          if (it > it0) {
+            if (!wait(&sm.kv_empty[(it - 1) & 1], (it - 1) >> 1)) break;  // O holds all tiles so far
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < Dv / 16; ++c) {
+              float o[16];
+              uint32_t w[2][8];
+              tmem_ld16(tmem + lane_base + kO + c * 16, o);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) w[e >> 3][e & 7] = __float_as_uint(o[e] * fix);
+              tmem_st8(tmem + lane_base + kO + c * 16, w[0]);
+              tmem_st8(tmem + lane_base + kO + c * 16 + 8, w[1]);
+            }
+            tmem_st_wait();
+          }
+        }
+        if (!ok) break;
+        l += sum;
+        tc_fence_before();
+        mbar_arrive(&sm.p_full[st]);
+      }
+      if (!ok) break;
+      // ---- the span's sums
+      if (!wait(&sm.kv_empty[(it - 1) & 1], (it - 1) >> 1)) break;
+      tc_fence_after();
+      const bool whole = cur.t0 == 0 && cur.t1 == cur.nt;
+      const int slot = 2 * blockIdx.x + (span > 1 ? 1 : 0);
+      if (cur.t0 == 0 && tid == 0)
+        a.ends[((int64_t)cur.b * v.Hkv + cur.hk) * a.nrb + cur.rb] = make_int2(slot, blockIdx.x + cur.parts_in - 1);
+      if (*reinterpret_cast<volatile int *>(&sm.bad[span & 3]) != span) {
+#pragma unroll 1
+        for (int c0 = 0; c0 < Dv; c0 += 64) {
+          float y[64];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            float o[16];
+            tmem_ld16(tmem + lane_base + kO + c0 + c * 16, o);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) y[c * 16 + e] = o[e];
+          }
+          if (!live) continue;
+#pragma unroll
+          for (int c = 0; c < 64; c += 4) {
+            const float back = 1.f / sm.unit[span & 3][(c0 + c) / 32];
+            float z[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) z[e] = y[column_of(c + e)] * back;
+            if (whole) {
+              finish_row<__nv_bfloat16>(a, cur.b, h, m, c0 + c, z, l, mx);
+            } else {
+              const int64_t at = (int64_t)slot * kTcRows + tid;
+              *reinterpret_cast<float4 *>(a.part + at * Dv + c0 + c) = make_float4(z[0], z[1], z[2], z[3]);
+              if (c0 + c == 0) *reinterpret_cast<float2 *>(a.part_ml + at * 2) = make_float2(mx, l);
+            }
+          }
+        }
+        tc_fence_before();
+      } else {
+        // a step outside what V' holds: the rows again, one warp a row
+        for (int r = warp; r < kTcRows; r += kSoftmaxWarps) {
+          const int gr2 = cur.rb * kTcRows + r;
+          const int m2 = gr2 / a.G, h2 = cur.hk * a.G + (gr2 - m2 * a.G);
+          if (m2 >= cur.rows) continue;
+          const __nv_bfloat16 *src =
+              (const __nv_bfloat16 *)a.Q.p + cur.b * a.Q.sb + h2 * a.Q.sh + m2 * a.Q.sn;
+          float *qs = sm.slow_q[warp];
+          __syncwarp();
+          for (int c = lane; c < D; c += 32) qs[c] = __bfloat162float(src[c]) * a.scale * 1.44269504f;
+          __syncwarp();
+          float mr, lr, o[NG];
+          slow_row<D, Dv>(a, v, cur.b, cur.hk, min(max(cur.len - cur.rows + m2 + 1, 0), cur.len), 4 * cur.t0,
+                          4 * cur.t1, qs, mr, lr, o);
+          const float at0 = mr == -CUDART_INF_F ? 0.f : mr;
+#pragma unroll
+          for (int k = 0; k < NG; ++k) {
+            const int c = 32 * k + lane;
+            if (whole) {
+              ((__nv_bfloat16 *)a.O.p + cur.b * a.O.sb + h2 * a.O.sh + m2 * a.O.sn)[c] =
+                  __float2bfloat16_rn(lr == 0.f ? 0.f : o[k] / lr);
+              if (c == 0 && a.lse)
+                a.lse[((int64_t)cur.b * a.H + h2) * a.M + m2] =
+                    lr == 0.f ? -CUDART_INF_F : (at0 + log2f(lr)) * 0.693147181f;
+            } else {
+              const int64_t at = (int64_t)slot * kTcRows + r;
+              a.part[at * Dv + c] = o[k];
+              if (c == 0) *reinterpret_cast<float2 *>(a.part_ml + at * 2) = make_float2(mr, lr);
+            }
+          }
+        }
+      }
+    }
+  }
+  // products still in flight land before shared memory and TMEM go: the last commit tracks them all
+  __syncthreads();
+  if (tid == kIssuer * 32) {
+    tc_commit(&sm.end);
+    mbar_drain(&sm.end, 0, status);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    __syncwarp();
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols)
+                 : "memory");
+  }
+}
+
+}  // namespace
+
+template <int D, int Dv>
+cudaError_t launch_attend_tc(AttendArgs a, const CacheView &v, int *status, cudaStream_t st) {
+  const auto kernel = attend_tc<D, Dv>;
+  const size_t smem = sizeof(Smem<D, Dv>) + 1024;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  int dev = 0, sms = 0;
+  if (e == cudaSuccess) e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  const int rows = a.G * a.M;
+  a.nrb = (rows + kTcRows - 1) / kTcRows;
+  a.min_tiles = 1;
+  a.tile_log2 = 7;
+  a.item_tiles = kTcItemTiles;
+  const int64_t items = (int64_t)a.B * v.Hkv * a.nrb;
+  const int64_t cap = (((int64_t)v.max_pages << v.page_log2) + kTok - 1) / kTok;
+  const int ctas = (int)std::min<int64_t>(std::min(sms, kTcMaxCtas), items * (cap + a.item_tiles));
+  e = launch_next(kernel, dim3(ctas), kThreads, smem, st, false, 0, a, v, status);
+  if (e != cudaSuccess) return e;
+  return launch_next(attend_join<__nv_bfloat16, Dv, kTcRows>, dim3(rows, v.Hkv, a.B), 128, 0, st, true,
+                     0, a, v, status);
+}
+
+template cudaError_t launch_attend_tc<64, 64>(AttendArgs, const CacheView &, int *, cudaStream_t);
+template cudaError_t launch_attend_tc<64, 128>(AttendArgs, const CacheView &, int *, cudaStream_t);
+template cudaError_t launch_attend_tc<128, 64>(AttendArgs, const CacheView &, int *, cudaStream_t);
+template cudaError_t launch_attend_tc<128, 128>(AttendArgs, const CacheView &, int *, cudaStream_t);
+
+}  // namespace muse

@@ -343,6 +343,9 @@ ATTEND = [  # B, H, Hkv, M, page, lens
     (1, 4, 2, 33, 64, [70]),
     (2, 8, 1, 128, 128, [128, 300]),
     (1, 3, 3, 65, 32, [40]),
+    (1, 1, 1, 65, 64, [65]),             # more than 64 rows: blocks of 128
+    (3, 8, 2, 20, 32, [0, 333, 130]),
+    (2, 6, 3, 100, 128, [1000, 99]),
     (1, 1, 1, 1, 1024, [5000]),
     (40, 2, 2, 1, 32, [(37 * i) % 257 for i in range(40)]),
 ]
