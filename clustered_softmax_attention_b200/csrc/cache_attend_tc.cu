@@ -9,8 +9,8 @@
 //                        when the running reference moves.
 // S of the next tile is issued before O += P V' of this one, so the softmax of one tile runs
 // beside both products.
-//   K' = code step 2^(12 - e), e the exponent of the token's largest step: exact while the token's
-//   groups are within 2^26 of each other; 2^(e - 12) multiplies the token's column of S.
+//   K' = code step 2^(12 - e), e the exponent of the largest step of sixteen tokens: exact for
+//   steps down to 2^-26 of that, off by 2^-37 of it below; 2^(e - 12) multiplies their columns of S.
 //   V' = code step unit[group], a power of two that the span's first tile sets; exact for steps
 //   from 2^-10 to 2^5 of its largest, and, zero steps apart, a tile with others makes the span go
 //   the slow way: its rows are computed again in float32 from the codes.
@@ -37,7 +37,7 @@ struct __align__(1024) Smem {
   __half v[2][Dv / 64][kTok * 64];
   // a producer's sixteen tokens as they are held: key codes, value codes, key steps, value steps
   uint8_t raw[kProducers][2][9 * (D + Dv)];
-  float tokf[2][kTok];        // what a token's column of S is multiplied by
+  float scale[2][kProducers]; // what sixteen tokens' columns of S are multiplied by
   float unit[4][Dv / 32];     // by span
   uint32_t big[2][kProducers][Dv / 64];  // by span
   float slow_q[kSoftmaxWarps][D];
@@ -262,107 +262,133 @@ attend_tc(const __grid_constant__ AttendArgs a, const __grid_constant__ CacheVie
         }
         if (it >= 2 && !wait(&sm.kv_empty[st], (it - 2) >> 1)) break;
         if (lane == 0) sm.gone[st][pw] = !here && base < cur.len;
-        // (loops, not unrolled: one warp a scheduler runs this, and straight code of its length
-        // would wait for its instructions)
-#pragma unroll 1
+        // ---- steps as float16.  Keys: the sixteen tokens' largest (a NaN is left out: it makes its
+        // token NaN) comes to exponent field 27; values: by the span's unit.
+        uint32_t top = 0;
+#pragma unroll
+        for (int w = 0; w < NGk / 2; ++w)
+          if (lane < n) top = __vmaxs2(top, reinterpret_cast<const uint32_t *>(raw + kRKS)[lane * (NGk / 2) + w]);
+        top = max(top & 0xffffu, top >> 16);
+#pragma unroll
+        for (int o = 8; o; o >>= 1) top = max(top, __shfl_xor_sync(kAll, top, o));
+        const int e_top = (int)(__shfl_sync(kAll, top, 0) >> 7);
+        if (lane == 0) sm.scale[st][pw] = ldexpf(1.f, e_top - 127 - 12);
+        const uint32_t k_shift = (uint32_t)((27 - e_top) * 128) * 0x10001u;
+        uint32_t ks[2][NGk / 2], vs[2][2][Dv / 64], off_range = 0;
+#pragma unroll
         for (int i = 0; i < 2; ++i) {
-          // ---- keys: row 8 i + g, a chunk of eight channels a word
-          {
-            const int row = pw * 16 + 8 * i + g;
-            const bool live = 8 * i + g < n;
-            uint32_t kw[NGk], ks[NGk / 2], top = 0;
-            if (D == 128) {
-              const uint4 x = reinterpret_cast<const uint4 *>(raw)[i * 32 + lane];
-              const uint2 y = reinterpret_cast<const uint2 *>(raw + kRKS)[8 * i + g];
-              kw[0] = x.x;
-              kw[1] = x.y;
-              kw[NGk - 2] = x.z;
-              kw[NGk - 1] = x.w;
-              ks[0] = y.x;
-              ks[NGk / 2 - 1] = y.y;
-            } else {
-              const uint2 x = reinterpret_cast<const uint2 *>(raw)[lane * 2 + i];
-              kw[0] = x.x;
-              kw[1] = x.y;
-              ks[0] = reinterpret_cast<const uint32_t *>(raw + kRKS)[8 * i + g];
-            }
-            bool nan = false;
+          if (D == 128) {
+            const uint2 y = reinterpret_cast<const uint2 *>(raw + kRKS)[8 * i + g];
+            ks[i][0] = y.x;
+            ks[i][NGk / 2 - 1] = y.y;
+          } else {
+            ks[i][0] = reinterpret_cast<const uint32_t *>(raw + kRKS)[8 * i + g];
+          }
+          if (Dv == 128) {
+            const uint4 y = reinterpret_cast<const uint4 *>(raw + kRVS)[4 * i + q];
+            vs[i][0][0] = y.x;
+            vs[i][0][Dv / 64 - 1] = y.y;
+            vs[i][1][0] = y.z;
+            vs[i][1][Dv / 64 - 1] = y.w;
+          } else {
+            const uint2 y = reinterpret_cast<const uint2 *>(raw + kRVS)[4 * i + q];
+            vs[i][0][0] = y.x;
+            vs[i][1][0] = y.y;
+          }
+          // fields 12..27 of keys, 8..23 of values (18: the first tile's largest); n < 16 also goes
+          // the careful way, for the tokens that are not there
 #pragma unroll
-            for (int w = 0; w < NGk / 2; ++w) {
-              if (!live) ks[w] = 0;
-              nan |= (ks[w] & 0x80008000u) != 0;
-              top = __vmaxu2(top, ks[w]);
-            }
-            const int e = (int)(max(top & 0xffffu, top >> 16) >> 7);
-            if (q == 0) sm.tokf[st][row] = !live ? 0.f : nan ? CUDART_NAN_F : ldexpf(1.f, e - 127 - 12);
+          for (int w = 0; w < NGk / 2; ++w) off_range |= ks[i][w] + k_shift - 0x06000600u;
 #pragma unroll
-            for (int w = 0; w < NGk; ++w) {
-              const int s = (int)((ks[w >> 1] >> (16 * (w & 1))) & 0xffffu);
-              const int f = s - (e - 27) * 128;  // exponent field at most 27
-              const bool keep = !nan && s >= 128 && f >= 128;
-              const __half2 step = __half2half2(__ushort_as_half(keep ? (unsigned short)(f << 3) : 0));
-              uint32_t c[4];
-              codes_f16(kw[w], c);
+          for (int w = 0; w < Dv / 64; ++w)
+            off_range |= (vs[i][0][w] + shift[w] - 0x04000400u) | (vs[i][1][w] + shift[w] - 0x04000400u);
+        }
+        if (__builtin_expect(!__any_sync(kAll, (off_range & 0xf800f800u) != 0) && n >= 16, 1)) {
 #pragma unroll
-              for (int k = 0; k < 4; ++k) c[k] = bits(__hmul2(*reinterpret_cast<__half2 *>(&c[k]), step));
-              *chunk(sm.k[st][w >> 1], row, (w & 1) * 4 + q) = make_uint4(c[0], c[1], c[2], c[3]);
+          for (int i = 0; i < 2; ++i) {
+#pragma unroll
+            for (int w = 0; w < NGk / 2; ++w) ks[i][w] = (ks[i][w] + k_shift) << 3;
+#pragma unroll
+            for (int w = 0; w < Dv / 64; ++w) {
+              vs[i][0][w] = (vs[i][0][w] + shift[w]) << 3;
+              vs[i][1][w] = (vs[i][1][w] + shift[w]) << 3;
             }
           }
-          // ---- values: rows 8 i + 2 q and + 1, chunk g: the word's eight channels
-          uint32_t vw[2][Dv / 64], vs[2][Dv / 64], off_range = 0;
+        } else {
+          // half by half: tokens that are not there and zero steps are zero; a key step too small is
+          // zero too, a NaN NaN; a value step that float16 does not hold sends the span the slow way
+#pragma unroll 1
+          for (int i = 0; i < 2; ++i) {
+            auto careful = [&](uint32_t x, uint32_t by, bool live, bool value) {
+              uint32_t d = 0;
+              const int low = (short)(by & 0xffffu), high = (short)((by - (uint32_t)low) >> 16);
+              for (int k = 0; k < 2; ++k) {
+                const int s = (int)((x >> (16 * k)) & 0xffffu), f = s + (k ? high : low);
+                if (!live || s == 0) continue;
+                if (value && (s >= 0x7f80 || f < 128 || f >= 28 * 128)) sm.bad[span & 3] = span;
+                else if (s >= 0x7f80) d |= 0x7e00u << (16 * k);
+                else if (s >= 128 && f >= 128) d |= (uint32_t)(f << 3) << (16 * k);
+              }
+              return d;
+            };
+            for (int w = 0; w < NGk / 2; ++w) {
+              const uint32_t d = careful(i ? ks[1][w] : ks[0][w], k_shift, 8 * i + g < n, false);
+              (i ? ks[1][w] : ks[0][w]) = d;
+            }
+            for (int e = 0; e < 2; ++e)
+              for (int w = 0; w < Dv / 64; ++w) {
+                const uint32_t d = careful(i ? vs[1][e][w] : vs[0][e][w], shift[w], 8 * i + 2 * q + e < n, true);
+                (i ? vs[1][e][w] : vs[0][e][w]) = d;
+              }
+          }
+        }
+        // ---- codes: keys to row 8 i + g, chunk (w % 2) 4 + q; values to rows 8 i + 2 q + e, chunk g
+        char *k_to = reinterpret_cast<char *>(sm.k[st][0]) + (pw * 16 + g) * 128;
+        char *v_to = reinterpret_cast<char *>(sm.v[st][0]) + (pw * 16 + 2 * q) * 128;
+        auto put = [&](char *to, uint32_t word, __half2 step) {
+          uint32_t c[4];
+          codes_f16(word, c);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) c[k] = bits(__hmul2(*reinterpret_cast<__half2 *>(&c[k]), step));
+          *reinterpret_cast<uint4 *>(to) = make_uint4(c[0], c[1], c[2], c[3]);
+        };
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          uint32_t kw[NGk], vw[2][Dv / 64];
+          if (D == 128) {
+            const uint4 x = reinterpret_cast<const uint4 *>(raw)[i * 32 + lane];
+            kw[0] = x.x;
+            kw[1] = x.y;
+            kw[NGk - 2] = x.z;
+            kw[NGk - 1] = x.w;
+          } else {
+            const uint2 x = reinterpret_cast<const uint2 *>(raw)[lane * 2 + i];
+            kw[0] = x.x;
+            kw[1] = x.y;
+          }
           if (Dv == 128) {
             const uint4 x = reinterpret_cast<const uint4 *>(raw + kRV)[i * 32 + lane];
-            const uint4 y = reinterpret_cast<const uint4 *>(raw + kRVS)[4 * i + q];
             vw[0][0] = x.x;
             vw[0][Dv / 64 - 1] = x.y;
             vw[1][0] = x.z;
             vw[1][Dv / 64 - 1] = x.w;
-            vs[0][0] = y.x;
-            vs[0][Dv / 64 - 1] = y.y;
-            vs[1][0] = y.z;
-            vs[1][Dv / 64 - 1] = y.w;
           } else {
             const uint2 x = reinterpret_cast<const uint2 *>(raw + kRV)[lane * 2 + i];
-            const uint2 y = reinterpret_cast<const uint2 *>(raw + kRVS)[4 * i + q];
             vw[0][0] = x.x;
             vw[1][0] = x.y;
-            vs[0][0] = y.x;
-            vs[1][0] = y.y;
+          }
+#pragma unroll
+          for (int w = 0; w < NGk; ++w) {
+            const __half2 two = *reinterpret_cast<__half2 *>(&ks[i][w >> 1]);
+            put(k_to + (w >> 1) * (kTok * 128) + i * 1024 + ((((w & 1) * 4 + q) ^ g) << 4), kw[w],
+                w & 1 ? __high2half2(two) : __low2half2(two));
           }
 #pragma unroll
           for (int e = 0; e < 2; ++e)
 #pragma unroll
-            for (int w = 0; w < Dv / 64; ++w)  // exponent fields 8..23, 18 the first tile's largest
-              if (8 * i + 2 * q + e < n) off_range |= vs[e][w] + shift[w] - 0x04000400u;
-          const bool odd = __any_sync(kAll, off_range & 0xf800f800u);
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int row = pw * 16 + 8 * i + 2 * q + e;
-            const bool live = 8 * i + 2 * q + e < n;
-#pragma unroll
-            for (int w = 0; w < Dv / 64; ++w) {
-              uint32_t d = (vs[e][w] + shift[w]) << 3;
-              if (__builtin_expect(odd, 0)) {
-                // half by half: a zero step is zero; a float16 from 2^-14 on will do; else slow
-                d = 0;
-                const int low = (short)(shift[w] & 0xffffu), high = (short)((shift[w] - (uint32_t)low) >> 16);
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                  const int s = (int)((vs[e][w] >> (16 * k)) & 0xffffu), f = s + (k ? high : low);
-                  if (!live || s == 0) continue;
-                  if (s >= 0x7f80 || f < 128 || f >= 28 * 128) sm.bad[span & 3] = span;
-                  else d |= (uint32_t)(f << 3) << (16 * k);
-                }
-              }
-              if (!live) d = 0;
-              uint32_t c[4];
-              codes_f16(vw[e][w], c);
-              const __half2 step = *reinterpret_cast<__half2 *>(&d);  // nibbles 0..3, 4..7
-#pragma unroll
-              for (int k = 0; k < 4; ++k) c[k] = bits(__hmul2(*reinterpret_cast<__half2 *>(&c[k]), step));
-              *chunk(sm.v[st][w], row, g) = make_uint4(c[0], c[1], c[2], c[3]);
-            }
-          }
+            for (int w = 0; w < Dv / 64; ++w)  // a step for nibbles 0..3, one for 4..7
+              put(v_to + w * (kTok * 128) + i * 1024 + e * 128 + ((g ^ (2 * q + e)) << 4), vw[e][w],
+                  *reinterpret_cast<__half2 *>(&vs[i][e][w]));
         }
         async_fence();
         mbar_arrive(&sm.kv_full[st]);
@@ -433,7 +459,7 @@ attend_tc(const __grid_constant__ AttendArgs a, const __grid_constant__ CacheVie
         top = max(top << 16, top & 0xffff0000u);
         const int e = min(max((int)(top >> 23) - 127 - 14, -114), 113);
         const float mul = top >= 0x7f800000u ? CUDART_NAN_F : a.scale < 0.f ? -ldexpf(1.f, -e) : ldexpf(1.f, -e);
-        rf = fmaxf(ldexpf(fabsf(a.scale) * 1.44269504f, e), 1e-37f);
+        rf = ldexpf(fabsf(a.scale) * 1.44269504f, e);
 #pragma unroll
         for (int i = 0; i < D / 8; ++i) {
           const uint4 x = live ? from[i] : make_uint4(0, 0, 0, 0);
@@ -452,7 +478,6 @@ attend_tc(const __grid_constant__ AttendArgs a, const __grid_constant__ CacheVie
         const uint32_t st = it & 1, col = tmem + lane_base + kS + st * 128;
         if (!wait(&sm.kv_full[st], it >> 1) || !wait(&sm.s_full[st], it >> 1)) break;
         tc_fence_after();
-        const float4 *tf = reinterpret_cast<const float4 *>(sm.tokf[st]);
         const int left = see - t * kTok;
         int gone = 0;
 #pragma unroll
@@ -466,42 +491,61 @@ attend_tc(const __grid_constant__ AttendArgs a, const __grid_constant__ CacheVie
           float top = -CUDART_INF_F;
           sum = 0.f;
           const float ref = mx == -CUDART_INF_F ? 0.f : mx;
-          uint32_t x[2][16];
-          tmem_ld16_async(col, x[0]);
+          float sums[2] = {0.f, 0.f};
+          // sixteen columns: c's weights from x
+          auto some = [&](int c, const uint32_t (&x)[16], bool masked) {
+            float y[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              y[e] = __uint_as_float(x[e]);
+              if (masked && (16 * c + e >= left || (gone >> c) & 1)) y[e] = -CUDART_INF_F;
+            }
+            const float to2 = fmaxf(sm.scale[st][c] * rf, 1e-37f);  // to logits in units of log 2
+            float m0 = fmaxf(y[0], y[1]), m1 = fmaxf(y[2], y[3]);
+#pragma unroll
+            for (int e = 4; e < 16; e += 4) {
+              m0 = fmaxf(m0, fmaxf(y[e], y[e + 1]));
+              m1 = fmaxf(m1, fmaxf(y[e + 2], y[e + 3]));
+            }
+            top = fmaxf(top, fmaxf(m0, m1) * to2);
+            uint32_t pk[8];
+#pragma unroll
+            for (int e = 0; e < 16; e += 2) {
+              const float p0 = ex2(fmaf(y[e], to2, -ref)), p1 = ex2(fmaf(y[e + 1], to2, -ref));
+              sums[(e >> 1) & 1] += p0 + p1;
+              pk[e >> 1] = pack_f16(p0, p1);
+            }
+            tmem_st8(tmem + lane_base + kP + st * 64 + c * 8, pk);
+          };
+          if (__builtin_expect(edge, 0)) {
 #pragma unroll 1
-          for (int c = 0; c < 8; c += 2) {
+            for (int c = 0; c < 8; ++c) {
+              uint32_t x[16];
+              tmem_ld16_async(col + c * 16, x);
+              arrived(x);
+              some(c, x, true);
+            }
+          } else {
+            uint32_t x[4][16];
+            tmem_ld16_async(col, x[0]);
+            tmem_ld16_async(col + 16, x[1]);
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
+            for (int c = 0; c < 8; c += 2) {
+              const int k = c & 2;
               arrived(x[k]);
-              if (c + k < 7) tmem_ld16_async(col + (c + k + 1) * 16, x[k ^ 1]);
-              float y[16];
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const float4 f = tf[4 * (c + k) + e];
-                y[4 * e] = __uint_as_float(x[k][4 * e]) * f.x;
-                y[4 * e + 1] = __uint_as_float(x[k][4 * e + 1]) * f.y;
-                y[4 * e + 2] = __uint_as_float(x[k][4 * e + 2]) * f.z;
-                y[4 * e + 3] = __uint_as_float(x[k][4 * e + 3]) * f.w;
+              arrived(x[k + 1]);
+              if (c < 6) {
+                tmem_ld16_async(col + (c + 2) * 16, x[k ^ 2]);
+                tmem_ld16_async(col + (c + 3) * 16, x[(k ^ 2) + 1]);
               }
-              if (__builtin_expect(edge, 0)) {
-#pragma unroll
-                for (int e = 0; e < 16; ++e)
-                  if (16 * (c + k) + e >= left || (gone >> (c + k)) & 1) y[e] = -CUDART_INF_F;
-              }
-              uint32_t pk[8];
-#pragma unroll
-              for (int e = 0; e < 16; e += 2) {
-                top = fmaxf(top, fmaxf(y[e], y[e + 1]));
-                const float p0 = ex2(fmaf(y[e], rf, -ref)), p1 = ex2(fmaf(y[e + 1], rf, -ref));
-                sum += p0 + p1;
-                pk[e >> 1] = pack_f16(p0, p1);
-              }
-              tmem_st8(tmem + lane_base + kP + st * 64 + (c + k) * 8, pk);
+              some(c, x[k], false);
+              some(c + 1, x[k + 1], false);
             }
           }
+          sum = sums[0] + sums[1];
           tmem_st_wait();
-          if (again || __builtin_expect(!__any_sync(kAll, top * rf > mx + 14.f), 1)) break;
-          const float now = fmaxf(mx, top * rf - 9.f);
+          if (again || __builtin_expect(!__any_sync(kAll, top > mx + 14.f), 1)) break;
+          const float now = fmaxf(mx, top - 9.f);
           const float fix = now == -CUDART_INF_F ? 1.f : ex2(mx - now);
           mx = now;
           l *= fix;
