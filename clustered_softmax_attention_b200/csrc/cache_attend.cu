@@ -26,7 +26,15 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kCluster = 8;      // CTAs of a cluster that takes an item
-constexpr int kClusterTiles = 16;  // of a token slice: the longest table that clusters take
+// Clusters take tables of up to so many 32-token tiles a token slice (a sequence's CTAs are fixed
+// beforehand, so a ragged batch waits for its longest): 8 sequence heads of 4000 tokens 18 us in
+// stretches, 12 here; 32 of 8000: 31 and 25, ragged 25 and 23; of 16000: 41 and 35, ragged 35 and 33,
+// but two of 16 heads 27 and 27.  Float32 rows, whose tiles take three times as long: 9 of 4000
+// tokens 18 and 14, of 8000 23 and 23, of 16000 27 and 33.  More CTAs than fit at once: 56 of 8000
+// tokens 37 and 45; only short tables then (56 of 1000: 23 either way).
+template <typename T>
+constexpr int kClusterTiles = sizeof(T) == 4 ? 32 : 64;
+constexpr int kClusterTilesTwice = 16;
 // ------------------------------------------------------------------ small device pieces
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void *src) {
@@ -300,12 +308,7 @@ attend(const __grid_constant__ AttendArgs a, const __grid_constant__ CacheView v
     walk.x = walk.x1 = 0;
     if (rank == 0 && sp.hk == 0 && sp.rb == 0 && tid == 0) check_lengths(a, v, sp.b, status);
   } else {
-    const int64_t total = line_total<kThreads>(a, v, run);
-    per = max((int64_t)a.min_tiles, (total + gridDim.x - 1) / gridDim.x);
-    walk.x = blockIdx.x * per;
-    walk.x1 = min(total, walk.x + per);
-    if (walk.x >= walk.x1) return;
-    line_find<kThreads>(a, v, run, walk.x, walk.b, walk.first);
+    if (!line_start<kThreads>(a, v, run, walk, per)) return;
     if (!next_span(a, v, walk, sp, per)) return;
   }
 
@@ -766,7 +769,8 @@ cudaError_t launch(AttendArgs a, const CacheView &v, int *status, cudaStream_t s
   a.item_tiles = kItemTiles;
   const int64_t items = (int64_t)a.B * v.Hkv * a.nrb;
   const int64_t cap = ((int64_t)v.max_pages << v.page_log2) / kTile;  // tiles a sequence can have
-  if (C::kClusters && cap <= kClusterTiles * C::kSlices && items * kCluster <= 2 * fit) {
+  if (C::kClusters && cap <= (items * kCluster <= fit ? kClusterTiles<T> : kClusterTilesTwice) * C::kSlices &&
+      items * kCluster <= 2 * fit) {
     a.cluster = (int)std::max<int64_t>(1, std::min<int64_t>(kCluster, (cap + C::kSlices - 1) / C::kSlices));
     return launch_next(kernel, dim3((unsigned)(items * a.cluster)), 32 * kWarps, C::kSmem, st,
                        true, a.cluster, a, v, status);

@@ -56,12 +56,7 @@ __device__ __forceinline__ int64_t seq_units(const AttendArgs &a, const CacheVie
   return nt ? (int64_t)(nt + a.item_tiles) * v.Hkv * a.nrb : 0;
 }
 
-// The line of tiles: its length, and the sequence in which position x lies with the position
-// of that sequence's first tile.  Each thread sums a run of sequences.
-struct Line {
-  int64_t total, first;
-  int b;
-};
+// The length of the line.  Each thread sums a run of sequences; run[t] is where thread t's ends.
 template <int kThreads>
 __device__ __forceinline__ int64_t line_total(const AttendArgs &a, const CacheView &v, int64_t *run) {
   const int tid = threadIdx.x, per = (a.B + kThreads - 1) / kThreads;
@@ -83,6 +78,7 @@ __device__ __forceinline__ int64_t line_total(const AttendArgs &a, const CacheVi
   __syncthreads();
   return run[kThreads - 1];
 }
+// The sequence in which position x lies, and the position of its first item.
 template <int kThreads>
 __device__ __forceinline__ void line_find(const AttendArgs &a, const CacheView &v,
                                           const int64_t *run, int64_t x, int &b, int64_t &first) {
@@ -133,11 +129,26 @@ static __device__ __noinline__ bool next_span(const AttendArgs &a, const CacheVi
     s.len = seq_len(a, v, w.b);
     s.rows = seq_rows(a, w.b);
     const int64_t left = w.x1 - start;  // tiles of the item up to this stretch's end
-    s.parts_in = left >= nt ? 1 : 1 + (int)((nt - left + per - 1) / per);
+    const uint32_t per32 = (uint32_t)min(per, (int64_t)0x7fffffff);
+    s.parts_in = left >= nt ? 1 : 1 + (int)(((uint32_t)(nt - left) + per32 - 1) / per32);
     w.x = left >= nt ? start + nt : w.x1;
     if (s.t0 < s.t1) return true;
   }
   return false;
+}
+
+// Places of a CTA's stretch, and where this one's begins; false when there is nothing left for it.
+template <int kThreads>
+__device__ __forceinline__ bool line_start(const AttendArgs &a, const CacheView &v, int64_t *run,
+                                           Walk &w, int64_t &per) {
+  const int64_t total = line_total<kThreads>(a, v, run);
+  const int64_t up = total + gridDim.x - 1;
+  per = max((int64_t)a.min_tiles, up >> 32 ? up / gridDim.x : (int64_t)((uint32_t)up / gridDim.x));
+  w.x = blockIdx.x * per;
+  w.x1 = min(total, w.x + per);
+  if (w.x >= w.x1) return false;
+  line_find<kThreads>(a, v, run, w.x, w.b, w.first);
+  return true;
 }
 
 __device__ __forceinline__ uint32_t bits(__half2 h) { return *reinterpret_cast<const uint32_t *>(&h); }

@@ -40,6 +40,7 @@ struct __align__(1024) Smem {
   float scale[2][kProducers]; // what sixteen tokens' columns of S are multiplied by
   float unit[4][Dv / 32];     // by span
   uint32_t big[2][kProducers][Dv / 64];  // by span
+  int exps[kTcRows];          // of the queries' powers of two
   float slow_q[kSoftmaxWarps][D];
   int bad[4];                 // number (from 1) of the last span that has to go the slow way
   int gone[2][kProducers];    // sixteen tokens that are not in the cache
@@ -144,14 +145,10 @@ attend_tc(const __grid_constant__ AttendArgs a, const __grid_constant__ CacheVie
   dependents_may_launch();
   wait_for_earlier();
 
-  const int64_t total = line_total<kThreads>(a, v, sm.run);
-  const int64_t per = max((int64_t)a.min_tiles, (total + gridDim.x - 1) / gridDim.x);
   Walk walk;
   Span sp;
-  walk.x = blockIdx.x * per;
-  walk.x1 = min(total, walk.x + per);
-  if (walk.x >= walk.x1) return;
-  line_find<kThreads>(a, v, sm.run, walk.x, walk.b, walk.first);
+  int64_t per;
+  if (!line_start<kThreads>(a, v, sm.run, walk, per)) return;
   if (!next_span(a, v, walk, sp, per)) return;
 
   if (tid == 0) {
@@ -444,31 +441,42 @@ attend_tc(const __grid_constant__ AttendArgs a, const __grid_constant__ CacheVie
       int see_all = see;
 #pragma unroll
       for (int x = 16; x; x >>= 1) see_all = min(see_all, __shfl_xor_sync(kAll, see_all, x));
-      // ---- the query as float16, a power of two a row: its largest in [2^14, 2^15)
-      float rf;
+      // ---- the queries as float16, a power of two a row: its largest in [2^14, 2^15).  A warp's 32
+      // rows, eight channels a lane at a time.
       {
-        const uint4 *from = reinterpret_cast<const uint4 *>(
-            (const __nv_bfloat16 *)a.Q.p + cur.b * a.Q.sb + h * a.Q.sh + m * a.Q.sn);
-        uint32_t top = 0;
+        constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes;
+        const int j = lane % kLanes;
+        uint4 all[32 / kAtOnce];
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
-          const uint4 x = live ? from[i] : make_uint4(0, 0, 0, 0);
-          top = __vmaxu2(__vmaxu2(top, x.x & 0x7fff7fffu), x.y & 0x7fff7fffu);
-          top = __vmaxu2(__vmaxu2(top, x.z & 0x7fff7fffu), x.w & 0x7fff7fffu);
+        for (int i = 0; i < 32 / kAtOnce; ++i) {
+          const int gr2 = cur.rb * kTcRows + warp * 32 + i * kAtOnce + lane / kLanes;
+          const int m2 = gr2 / a.G, h2 = cur.hk * a.G + (gr2 - m2 * a.G);
+          all[i] = make_uint4(0, 0, 0, 0);
+          if (m2 < cur.rows)
+            all[i] = reinterpret_cast<const uint4 *>((const __nv_bfloat16 *)a.Q.p + cur.b * a.Q.sb +
+                                                     h2 * a.Q.sh + m2 * a.Q.sn)[j];
         }
-        top = max(top << 16, top & 0xffff0000u);
-        const int e = min(max((int)(top >> 23) - 127 - 14, -114), 113);
-        const float mul = top >= 0x7f800000u ? CUDART_NAN_F : a.scale < 0.f ? -ldexpf(1.f, -e) : ldexpf(1.f, -e);
-        rf = ldexpf(fabsf(a.scale) * 1.44269504f, e);
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
-          const uint4 x = live ? from[i] : make_uint4(0, 0, 0, 0);
+        for (int i = 0; i < 32 / kAtOnce; ++i) {
+          const int r = warp * 32 + i * kAtOnce + lane / kLanes;
+          const uint4 x = all[i];
+          uint32_t top = __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu),
+                                  __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu));
+          top = max(top << 16, top & 0xffff0000u);
+#pragma unroll
+          for (int o = 1; o < kLanes; o <<= 1) top = max(top, __shfl_xor_sync(kAll, top, o));
+          const int e = min(max((int)(top >> 23) - 127 - 14, -114), 113);
+          const float up = __uint_as_float((uint32_t)(127 - e) << 23);  // 2^-e, a normal number
+          const float mul = top >= 0x7f800000u ? CUDART_NAN_F : a.scale < 0.f ? -up : up;
+          if (j == 0) sm.exps[r] = e;
           // channels (0, 4), (1, 5), (2, 6), (3, 7) of eight
-          *chunk(sm.q[i / 8], tid, i % 8) =
+          *chunk(sm.q[j / 8], r, j % 8) =
               make_uint4(pack_f16(lo_f(x.x) * mul, lo_f(x.z) * mul), pack_f16(hi_f(x.x) * mul, hi_f(x.z) * mul),
                          pack_f16(lo_f(x.y) * mul, lo_f(x.w) * mul), pack_f16(hi_f(x.y) * mul, hi_f(x.w) * mul));
         }
+        __syncwarp();
       }
+      const float rf = ldexpf(fabsf(a.scale) * 1.44269504f, sm.exps[tid]);
       async_fence();
       mbar_arrive(&sm.q_full);
 
