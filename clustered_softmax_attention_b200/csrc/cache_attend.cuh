@@ -11,6 +11,8 @@
 namespace muse {
 
 constexpr int kMaxCtas = 592;   // 148 SMs x 4: the bound of the partials in the workspace
+constexpr int kTcRows = 128;    // rows of a block of the form for many rows
+constexpr int kTcMaxCtas = 160; // its CTAs: one an SM
 struct AttendArgs {
   muse_rows Q, O;
   float *lse;
@@ -228,6 +230,12 @@ __global__ void __launch_bounds__(128) attend_join(const AttendArgs a, const Cac
   const int2 ends = nt ? a.ends[item] : make_int2(0, -1);
   const int c0 = ends.x >> 1, n = ends.y - c0 + 1;
   if (n == 1) return;  // finished by its only CTA
+  // a wait that gave up leaves an item without its ends: nothing is read by them
+  constexpr int kCtas = kRows == kTcRows ? kTcMaxCtas : kMaxCtas;
+  if (nt && ((unsigned)c0 >= (unsigned)kCtas || (unsigned)ends.y >= (unsigned)kCtas || n < 1)) {
+    if (tid == 0) report(status, MUSE_ERR_DEVICE);
+    return;
+  }
   // a part that begins its stretch is in the even slot: all but, perhaps, the first
   auto slot_of = [&](int k) { return k ? 2 * (int64_t)(c0 + k) : (int64_t)ends.x; };
   float ref = -CUDART_INF_F;
@@ -278,8 +286,6 @@ __global__ void __launch_bounds__(128) attend_join(const AttendArgs a, const Cac
 }
 
 // The form for more than 64 bfloat16 rows of a cache head (cache_attend_tc.cu), in blocks of 128.
-constexpr int kTcRows = 128;
-constexpr int kTcMaxCtas = 160;    // one an SM
 constexpr int kTcItemTiles = 3;  // beginning and ending an item, in tiles of 128 tokens
 template <int D, int Dv>
 cudaError_t launch_attend_tc(AttendArgs a, const CacheView &v, int *status, cudaStream_t st);

@@ -623,3 +623,86 @@ def test_launch_counter_counts_the_serving_kernels():
     m.muse_cache_read(s.cache, s.table, ints([0]), 40, 64)
     m.muse_cache_attend(Q, s.cache, s.table, ints([40]))
     assert lib.muse_launch_counter() - n0 >= 3
+
+
+def test_a_replayed_chunk_of_many_rows_follows_the_lengths():
+    """The form for many rows, captured: two graphs over one workspace, lengths and counts updated
+    in place, a sequence with fewer rows than the others and one with none."""
+    B, H, Hkv, M, D = 3, 8, 2, 40, 64
+    s = filled(B, Hkv, 32, 20, D, D, 600)
+    Q = randn(4, B, H, M, D, dtype=BF16)
+    lens, counts = ints([600, 300, 40]), ints([M, 1, 0])
+    out, lse = torch.zeros_like(Q), torch.zeros(B, H, M, device="cuda")
+    ws = m.workspace("muse_cache_attend", m.dims(Q), Hkv)
+    call = lambda: m.muse_cache_attend(Q, s.cache, s.table, lens, counts=counts, scale=0.125,
+                                       out=out, lse=lse, ws=ws)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        call()
+    torch.cuda.current_stream().wait_stream(side)
+    graphs = []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            call()
+        graphs.append(g)
+    for i, (ln, cn) in enumerate((([599, 41, 40], [40, 1, 0]), ([7, 513, 1], [0, 40, 1]),
+                                  ([128, 129, 600], [17, 33, 40]), ([600, 300, 40], [40, 1, 0]))):
+        lens.copy_(ints(ln))
+        counts.copy_(ints(cn))
+        Q.copy_(randn(50 + i, *Q.shape, dtype=BF16))
+        out.fill_(7.0)
+        graphs[i % 2].replay()
+        attend_close(host(out), host(lse), Q, s, ln, cn, 0.125, BF16)
+        assert all((out[b, :, cn[b]:] == 7.0).all() for b in range(B))
+    ok()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_pages_past_four_gigabytes(dtype):
+    """A cache of 15000 pages (4.4 GB), the sequence's pages at both ends of it: what is written,
+    read and attended is what a small cache gives."""
+    mp, Hkv, page, D = 3, 2, 1024, 128
+    small = Store(1, Hkv, page, mp, D, D)
+    big = torch.empty(m.muse_cache_shape(15000, Hkv, page, D, D), dtype=torch.uint8, device="cuda")
+    assert big.numel() > 2 ** 32
+    table = ints([[14999, 0, 14600]])
+    T = mp * page - 5
+    K, V = (randn(i, 1, Hkv, T, D, dtype=dtype) for i in (1, 2))
+    got = []
+    for cache, tab in ((small.cache, small.table), (big, table)):
+        m.muse_cache_write(cache, K, V, tab, ints([0]))
+        r = list(m.muse_cache_read(cache, tab, ints([0]), T, D, dtype=dtype))
+        for H, M in ((4, 1), (8, 40)):
+            r += m.muse_cache_attend(randn(3, 1, H, M, D, dtype=dtype), cache, tab, ints([T]), scale=0.1)
+        got.append(r)
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+    ok()
+
+
+@pytest.mark.parametrize("M", [1, 40])
+def test_sequences_that_share_pages(M):
+    """A common beginning in the same pages, read by all."""
+    s = filled(3, 2, 32, 12, 64, 64, 380)
+    s.table_np[1:, :8] = s.table_np[0, :8]
+    s.table = ints(s.table_np)
+    lens = [380, 256, 300]
+    Q = randn(5, 3, 8, M, 64, dtype=BF16)
+    out, lse = m.muse_cache_attend(Q, s.cache, s.table, ints(lens), scale=0.125)
+    attend_close(host(out), host(lse), Q, s, lens, [M] * 3, 0.125, BF16)
+    ok()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("H,M", [(2, 128), (16, 40), (64, 5)])
+def test_a_padded_batch_of_one_long_chunk_and_single_tokens(H, M, dtype):
+    """Several row blocks a head, of which most sequences use one."""
+    B = 6
+    s = filled(B, 2, 64, 10, 64, 64, 600)
+    lens, counts = [600, 33, 1, 599, 0, 64], [M, 1, 1, 2, 1, 0]
+    Q = randn(5, B, H, M, 64, dtype=dtype)
+    out, lse = m.muse_cache_attend(Q, s.cache, s.table, ints(lens), ints(counts), scale=0.125)
+    attend_close(host(out), host(lse), Q, s, lens, counts, 0.125, dtype)
+    assert all((out[b, :, counts[b]:] == 0).all() for b in range(B))
+    ok()
