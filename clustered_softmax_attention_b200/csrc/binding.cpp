@@ -177,7 +177,9 @@ PyObject *rope_axes(PyObject *const *a) {
   Py_DECREF(seq);
   r.axes = (int)axes;
   r.base = real(a[3], "base");
-  r.flags = (unsigned)whole(a[5], "flags");
+  const int64_t flags = whole(a[5], "flags");
+  if (flags < 0 || flags > (int64_t)UINT32_MAX) refuse("flags", "unknown flags ", flags);
+  r.flags = (unsigned)flags;
   const bool shared = pos.dim() == 2;
   const int32_t *p = shared ? ints(pos, "positions", {axes, f.N}, f.device)
                             : ints(pos, "positions", {f.B, axes, f.N}, f.device);

@@ -202,3 +202,11 @@ def test_binding_refuses_overlapping_rows_on_the_gpu():
         m.muse_rope_axes(x, pos, [33])
     with pytest.raises(m.MuseError, match="SHAPE"):
         m.muse_rope_axes(x[..., :32].contiguous(), pos, [8])
+
+
+@pytest.mark.parametrize("flags", [2 ** 32, 2 ** 32 + 1, -1, -2 ** 40])
+def test_binding_does_not_cut_flags_short(flags):
+    """2^32 is no flag, nor is it none."""
+    x = torch.zeros(2, 4, 8, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="flags"):
+        m.muse_rope_axes(x, torch.zeros(1, 8, dtype=torch.int32), [32], flags=flags)
