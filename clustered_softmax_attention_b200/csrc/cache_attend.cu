@@ -300,7 +300,7 @@ attend(const __grid_constant__ AttendArgs a, const __grid_constant__ CacheView v
     sp.b = item / (v.Hkv * a.nrb);
     sp.hk = item / a.nrb % v.Hkv;
     sp.rb = item % a.nrb;
-    sp.nt = seq_tiles(a, v, sp.b);
+    sp.nt = sp.rb < seq_blocks(a, sp.b) ? seq_tiles(a, v, sp.b) : 0;
     sp.t0 = sp.nt * rank / a.cluster;
     sp.t1 = sp.nt * (rank + 1) / a.cluster;
     sp.len = seq_len(a, v, sp.b);
@@ -421,7 +421,8 @@ attend(const __grid_constant__ AttendArgs a, const __grid_constant__ CacheView v
       for (int k = 0; k < 2; ++k) {
         rf[nb][k] = __shfl_sync(kAll, rfg, (2 * q + k) * 4);
         const int m = (row0 + 2 * q + k) / a.G;
-        see[nb][k] = m < sp.rows ? min(max(sp.len - sp.rows + m + 1, 0), sp.len) : 0;
+        // a place without a row sees all, so that it masks nothing for its tile (it is not written)
+        see[nb][k] = m < sp.rows ? min(max(sp.len - sp.rows + m + 1, 0), sp.len) : sp.len;
         see_all = min(see_all, see[nb][k]);
       }
 #pragma unroll
@@ -764,6 +765,7 @@ cudaError_t launch(AttendArgs a, const CacheView &v, int *status, cudaStream_t s
   }
   const int rows = a.G * a.M;
   a.nrb = (rows + C::kRows - 1) / C::kRows;
+  a.block_log2 = C::kRows == 8 ? 3 : C::kRows == 16 ? 4 : C::kRows == 32 ? 5 : 6;
   a.min_tiles = C::kSlices;
   a.tile_log2 = 5;
   a.item_tiles = kItemTiles;
@@ -834,7 +836,7 @@ cudaError_t run_cache_attend(const muse_rows &Q, const muse_dims &d, const muse_
   a.H = d.H;
   a.M = d.N;
   a.G = d.H / c.Hkv;
-  a.nrb = a.min_tiles = a.tile_log2 = a.item_tiles = a.cluster = 0;
+  a.nrb = a.block_log2 = a.min_tiles = a.tile_log2 = a.item_tiles = a.cluster = 0;
   a.scale = d.scale;
   const AttendWs w(d.B, d.H, d.N, d.Dv, c.Hkv, d.dtype);
   char *p = static_cast<char *>(ws);

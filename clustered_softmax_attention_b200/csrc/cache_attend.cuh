@@ -18,7 +18,8 @@ struct AttendArgs {
   float *lse;
   const int32_t *lens, *counts;
   int B, H, M, G;      // G = H / Hkv
-  int nrb;             // row blocks of an item's G * M rows
+  int nrb;             // row blocks of a head's G * M rows, 2^block_log2 rows each
+  int block_log2;
   int min_tiles;       // a CTA takes at least so many tiles
   int tile_log2;       // tokens of a tile: 32, or 128
   int item_tiles;      // kItemTiles, in such tiles
@@ -53,9 +54,13 @@ __device__ __forceinline__ int seq_tiles(const AttendArgs &a, const CacheView &v
 // tokens, 8 heads: 182 us with 0, 93 with 6 and 10, 81 with 16; as many tokens in sequences of
 // one length: 79.
 constexpr int kItemTiles = 16;
+// Row blocks of sequence b: a padded batch has sequences with fewer rows than M.
+__device__ __forceinline__ int seq_blocks(const AttendArgs &a, int b) {
+  return (a.G * seq_rows(a, b) + (1 << a.block_log2) - 1) >> a.block_log2;
+}
 __device__ __forceinline__ int64_t seq_units(const AttendArgs &a, const CacheView &v, int b) {
   const int nt = seq_tiles(a, v, b);
-  return nt ? (int64_t)(nt + a.item_tiles) * v.Hkv * a.nrb : 0;
+  return nt ? (int64_t)(nt + a.item_tiles) * v.Hkv * seq_blocks(a, b) : 0;
 }
 
 // The length of the line.  Each thread sums a run of sequences; run[t] is where thread t's ends.
@@ -123,8 +128,9 @@ static __device__ __noinline__ bool next_span(const AttendArgs &a, const CacheVi
     const int item = in >> 32 ? (int)(in / one) : (int)((uint32_t)in / one);
     const int64_t start = w.first + (int64_t)item * one + a.item_tiles;  // of its tiles
     s.b = w.b;
-    s.hk = item / a.nrb;
-    s.rb = item - s.hk * a.nrb;
+    const int blocks = seq_blocks(a, w.b);
+    s.hk = item / blocks;
+    s.rb = item - s.hk * blocks;
     s.nt = nt;
     s.t0 = (int)max((int64_t)0, w.x - start);
     s.t1 = (int)max((int64_t)0, min((int64_t)nt, w.x1 - start));

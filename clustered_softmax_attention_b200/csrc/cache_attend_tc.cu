@@ -437,7 +437,8 @@ attend_tc(const __grid_constant__ AttendArgs a, const __grid_constant__ CacheVie
       const int gr = cur.rb * kTcRows + tid;
       const int m = gr / a.G, h = cur.hk * a.G + (gr - m * a.G);
       const bool live = m < cur.rows;
-      const int see = live ? min(max(cur.len - cur.rows + m + 1, 0), cur.len) : 0;
+      // a place without a row sees all, so that it masks nothing for its warp (it is not written)
+      const int see = live ? min(max(cur.len - cur.rows + m + 1, 0), cur.len) : cur.len;
       int see_all = see;
 #pragma unroll
       for (int x = 16; x; x >>= 1) see_all = min(see_all, __shfl_xor_sync(kAll, see_all, x));
@@ -678,6 +679,7 @@ cudaError_t launch_attend_tc(AttendArgs a, const CacheView &v, int *status, cuda
   if (e != cudaSuccess) return e;
   const int rows = a.G * a.M;
   a.nrb = (rows + kTcRows - 1) / kTcRows;
+  a.block_log2 = 7;
   a.min_tiles = 1;
   a.tile_log2 = 7;
   a.item_tiles = kTcItemTiles;
