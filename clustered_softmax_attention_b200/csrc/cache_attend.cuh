@@ -50,10 +50,10 @@ __device__ __forceinline__ int seq_tiles(const AttendArgs &a, const CacheView &v
 }
 
 // Beginning and ending an item (its queries, joining its sums) takes a CTA as long as kItemTiles
-// tiles: so many places on the line come before each item's tiles.  48 sequences of 0 to 8192
-// tokens, 8 heads: 182 us with 0, 93 with 6 and 10, 81 with 16; as many tokens in sequences of
-// one length: 79.
-constexpr int kItemTiles = 16;
+// tiles: so many places on the line come before each item's tiles.  With 8, 12, 16, 20 and 28: 48
+// sequences of up to 8192 tokens, 8 heads, 91 81 76 71 74 us; 64 of up to 4096 with 16 rows a head,
+// 102 92 88 84 85; 200 of up to 2048, 119 115 105 102 100; 2 of 65536, 16 heads, 82 80.5 80 79.5 79.
+constexpr int kItemTiles = 20;
 // Row blocks of sequence b: a padded batch has sequences with fewer rows than M.
 __device__ __forceinline__ int seq_blocks(const AttendArgs &a, int b) {
   return (a.G * seq_rows(a, b) + (1 << a.block_log2) - 1) >> a.block_log2;
