@@ -213,81 +213,92 @@ __device__ __forceinline__ void finish_row(const AttendArgs &a, int b, int h, in
         z == 0.f ? -CUDART_INF_F : (at + log2f(z)) * 0.693147181f;
 }
 
-// Rows of items that lie in several stretches (or in none: nothing to see).  One CTA per row: the
-// weights of all parts first, then their sums by four warps in turn, all loads independent, joined
-// in a fixed order.
+// Rows of items that lie in several stretches (or in none: nothing to see).  One CTA per row, its
+// parts read by four warps in turn and joined in a fixed order.  It is as long as its loads that
+// wait for one another: the ends, then references and sums together.
 template <typename T, int Dv, int kRows>
-__global__ void __launch_bounds__(128) attend_join(const AttendArgs a, const CacheView v,
-                                                   int *status) {
-  constexpr int kThreads = 128, kGroups = kThreads / (Dv / 4);
-  __shared__ float s_w[kMaxCtas], s_red[8];
+__global__ void __launch_bounds__(128, 12) attend_join(const __grid_constant__ AttendArgs a,
+                                                   const __grid_constant__ CacheView v, int *status) {
+  constexpr int kThreads = 128, kGroups = kThreads / (Dv / 4), kAhead = 4;
+  constexpr int kCtas = kRows == kTcRows ? kTcMaxCtas : kMaxCtas;
+  constexpr int kMine = (kCtas + kThreads - 1) / kThreads;  // references of a thread
+  __shared__ float s_w[kCtas], s_red[8];
   __shared__ float4 s_y[kGroups][Dv / 4];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int gr = blockIdx.x, hk = blockIdx.y, b = blockIdx.z;
+  const int m = gr / a.G, h = hk * a.G + (gr - m * a.G);
+  const int rb = gr / kRows, row = gr - rb * kRows;
   dependents_may_launch();
   wait_for_earlier();
+  int2 ends = a.ends[((int64_t)b * v.Hkv + hk) * a.nrb + rb];  // not written where there is nothing
   const int rows = seq_rows(a, b);
   if (gr == 0 && hk == 0 && tid == 0) check_lengths(a, v, b, status);
-  const int m = gr / a.G, h = hk * a.G + (gr - m * a.G);
-  const int nt = m < rows ? seq_tiles(a, v, b) : 0;
+  const int nt = seq_tiles(a, v, b);
   if (m >= rows) return;
-  const int rb = gr / kRows, row = gr - rb * kRows;
-  const int64_t item = ((int64_t)b * v.Hkv + hk) * a.nrb + rb;
-  const int2 ends = nt ? a.ends[item] : make_int2(0, -1);
+  if (!nt) ends = make_int2(0, -1);
   const int c0 = ends.x >> 1, n = ends.y - c0 + 1;
   if (n == 1) return;  // finished by its only CTA
   // a wait that gave up leaves an item without its ends: nothing is read by them
-  constexpr int kCtas = kRows == kTcRows ? kTcMaxCtas : kMaxCtas;
   if (nt && ((unsigned)c0 >= (unsigned)kCtas || (unsigned)ends.y >= (unsigned)kCtas || n < 1)) {
     if (tid == 0) report(status, MUSE_ERR_DEVICE);
     return;
   }
   // a part that begins its stretch is in the even slot: all but, perhaps, the first
   auto slot_of = [&](int k) { return k ? 2 * (int64_t)(c0 + k) : (int64_t)ends.x; };
-  float ref = -CUDART_INF_F;
-  for (int k = tid; k < n; k += kThreads) {
-    const int64_t slot = slot_of(k);
-    s_w[k] = a.part_ml[(slot * kRows + row) * 2];
-    ref = fmaxf(ref, s_w[k]);
+  const int grp = tid / (Dv / 4), c4 = tid - grp * (Dv / 4);
+  auto part = [&](int k) {
+    return reinterpret_cast<const float4 *>(a.part + (slot_of(k) * kRows + row) * Dv)[c4];
+  };
+  float2 ml[kMine];
+#pragma unroll
+  for (int i = 0; i < kMine; ++i) {
+    const int k = tid + i * kThreads;
+    ml[i] = make_float2(-CUDART_INF_F, 0.f);
+    if (k < n) ml[i] = *reinterpret_cast<const float2 *>(a.part_ml + (slot_of(k) * kRows + row) * 2);
   }
+  float4 first[kAhead];
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) {
+    first[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (grp + i * kGroups < n) first[i] = part(grp + i * kGroups);
+  }
+  float ref = -CUDART_INF_F;
+#pragma unroll
+  for (int i = 0; i < kMine; ++i) ref = fmaxf(ref, ml[i].x);
   ref = warp_max(ref);
   if (lane == 0) s_red[warp] = ref;
   __syncthreads();
   ref = fmaxf(fmaxf(s_red[0], s_red[1]), fmaxf(s_red[2], s_red[3]));
   const float at = ref == -CUDART_INF_F ? 0.f : ref;
   float z = 0.f;
-  for (int k = tid; k < n; k += kThreads) {
-    const int64_t slot = slot_of(k);
-    s_w[k] = ex2(s_w[k] - at);
-    z = fmaf(s_w[k], a.part_ml[(slot * kRows + row) * 2 + 1], z);
+#pragma unroll
+  for (int i = 0; i < kMine; ++i) {
+    const int k = tid + i * kThreads;
+    const float w = ex2(ml[i].x - at);
+    if (k < n) s_w[k] = w;
+    z = fmaf(w, ml[i].y, z);
   }
   z = warp_sum(z);
   if (lane == 0) s_red[4 + warp] = z;
   __syncthreads();
   z = (s_red[4] + s_red[5]) + (s_red[6] + s_red[7]);
-  const int grp = tid / (Dv / 4), c4 = tid - grp * (Dv / 4);
   float y[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 8
-  for (int k = grp; k < n; k += kGroups) {
-    const int64_t slot = slot_of(k);
-    const float4 o = reinterpret_cast<const float4 *>(a.part + (slot * kRows + row) * Dv)[c4];
-    const float f = s_w[k];
+  auto add = [&](float f, const float4 &o) {
     y[0] = fmaf(f, o.x, y[0]);
     y[1] = fmaf(f, o.y, y[1]);
     y[2] = fmaf(f, o.z, y[2]);
     y[3] = fmaf(f, o.w, y[3]);
-  }
+  };
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i)
+    if (grp + i * kGroups < n) add(s_w[grp + i * kGroups], first[i]);
+#pragma unroll 8
+  for (int k = grp + kAhead * kGroups; k < n; k += kGroups) add(s_w[k], part(k));
   s_y[grp][c4] = make_float4(y[0], y[1], y[2], y[3]);
   __syncthreads();
   if (grp) return;
 #pragma unroll
-  for (int k = 1; k < kGroups; ++k) {
-    const float4 o = s_y[k][c4];
-    y[0] += o.x;
-    y[1] += o.y;
-    y[2] += o.z;
-    y[3] += o.w;
-  }
+  for (int k = 1; k < kGroups; ++k) add(1.f, s_y[k][c4]);
   finish_row<T>(a, b, h, m, 4 * c4, y, z, at);
 }
 
