@@ -20,8 +20,8 @@
 // What bounds it, bfloat16 rows of 128 + 128 channels: up to 8 rows a cache head a 32-token tile
 // costs the card 0.9 ns, 5.2 TB/s of codes (79 % of a copy's rate); it is the instructions that
 // turn codes into operands (660 a tile; ALU 43 %, tensor pipe 22 %, issue slots about half used), not DRAM
-// (48 %).  Two sequences of 65536 tokens, 16 heads: 80 us, of which 60 are tiles and 20 are not:
-// setting up, the first tile's way, 8 us of joining.  8 x 8 heads of 32768 tokens: 86 us with up to 8
+// (48 %).  Two sequences of 65536 tokens, 16 heads: 79 us, of which 59 are tiles and 20 are not:
+// setting up, the first tile's way, 7 us of joining.  8 x 8 heads of 32768 tokens: 86 us with up to 8
 // rows, 109 with 16, 199 with 32, 358 with 64: codes are dequantised by every warp for its 16 rows.
 #include <algorithm>
 #include <atomic>

@@ -18,7 +18,7 @@
 // four apart a register; Q is laid out alike, and the output's columns are put back at the end.
 //
 // Two sequences, two cache heads of four query heads, 128 new rows (512 rows a cache head), 128 + 128
-// channels: 57 us over 16384 tokens, of which about 25 are a call's beginning and end; from there
+// channels: 55 us over 16384 tokens, of which about 23 are a call's beginning and end; from there
 // 16 ns a tile of 128 x 128 (2.4 us an SM), 524 TFLOP/s of 1640: both products are 0.8 of those 2.4 us,
 // and the way of a tile through the three roles is the rest (ALU 23 %, exponentials 17 %, no unit is
 // busy).  Eight softmax warps instead of four, and an issuer among the producers, gained nothing.
