@@ -320,7 +320,9 @@ muse_status muse_backward(const void *Q, const void *K, const void *V, const voi
  * Rows are given by a view: the element (b, h, n, c) of a tensor is at
  * p + (b*sb + h*sh + n*sn + c) * element size.  p is 16-byte aligned and every stride a
  * multiple of 16 bytes (so a projection's [B,N,H,D] output is read where it is); for what is
- * read a stride may be 0 (a broadcast tensor), rows that are written must not overlap.
+ * read a stride may be 0 (a broadcast tensor), rows that are written must not overlap.  What a
+ * call writes must not overlap what it reads, rotary positions in place apart.  N = 0 and other
+ * widths than 64 and 128 are refused.
  */
 typedef struct {
   void *p;            /* not written through where the argument is an input */
@@ -413,7 +415,8 @@ muse_status muse_cache_read(muse_dims d, muse_cache c, const int32_t *start, con
  * or NULL.  The codes enter the products as they are (integers), the steps in float32.
  * A length below 0 or past the table, or a page outside the cache, sets MUSE_ERR_DEVICE; those
  * tokens are left out.  Workspace: muse_workspace_size("muse_cache_attend", d, c.Hkv, ...); the
- * library leaves nothing in it that the next call needs.
+ * library leaves nothing in it that the next call needs; calls that may run at the same time need
+ * one each.  A call repeats bit for bit.
  */
 #define MUSE_CACHE_MAX_ROWS 128
 muse_status muse_cache_attend(muse_rows Q, muse_dims d, muse_cache c, const int32_t *lens,
