@@ -399,6 +399,7 @@ attend_tc(const __grid_constant__ AttendArgs a, const __grid_constant__ CacheVie
                   *reinterpret_cast<__half2 *>(&vs[i][e][w]));
         }
         async_fence();
+        __syncwarp();  // all lanes have read raw[st]: the next fetch writes there
         mbar_arrive(&sm.kv_full[st]);
       }
     }
