@@ -2,6 +2,10 @@
 
 Tolerances are worst-case bounds written beside each comparison: u = 2^-24 is half a float32
 step, h = 2^-8 half a bfloat16 step (relative)."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -706,3 +710,38 @@ def test_a_padded_batch_of_one_long_chunk_and_single_tokens(H, M, dtype):
     attend_close(host(out), host(lse), Q, s, lens, counts, 0.125, dtype)
     assert all((out[b, :, counts[b]:] == 0).all() for b in range(B))
     ok()
+
+
+FIRST_CALL = """
+import torch
+from clustered_softmax_attention_b200 import muse as m
+H, M = {H}, {M}
+cache = torch.zeros(m.muse_cache_shape(4, 2, 64, 64, 64), dtype=torch.uint8, device="cuda")
+table = torch.arange(4, dtype=torch.int32, device="cuda").view(1, 4)
+K = torch.ones(1, 2, 200, 64, device="cuda", dtype=torch.bfloat16)
+Q = torch.ones(1, H, M, 64, device="cuda", dtype=torch.bfloat16)
+pos = torch.zeros(1, M, dtype=torch.int32, device="cuda")
+zero, lens = torch.zeros(1, dtype=torch.int32, device="cuda"), torch.full((1,), 200, dtype=torch.int32, device="cuda")
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    m.muse_cache_write(cache, K, K, table, zero)
+    q = m.muse_rope_axes(Q, pos, [32])
+    out, lse = m.muse_cache_attend(q, cache, table, lens, scale=0.125)
+g.replay()
+torch.cuda.synchronize()
+want = float(torch.tensor(1 / 7, dtype=torch.bfloat16)) * 7
+assert (out.float() - want).abs().max() <= want * (2 ** -8 + 2 ** -9), out
+assert m.muse_last_device_status() == 0
+print("replayed")
+"""
+
+
+@pytest.mark.parametrize("H,M", [(4, 1), (8, 40)])
+def test_the_first_calls_of_a_process_are_captured(H, M):
+    """What is looked up once a device is looked up during the capture.  Every value is code 7 of
+    the step bf16(1/7) and the weights sum to one: off by the result's half step 2^-8 and weights
+    of 11 bits, once for p and once for p step (2^-11 each), and float32 sums: below 2^-9."""
+    r = subprocess.run([sys.executable, "-c", FIRST_CALL.format(H=H, M=M)], capture_output=True, text=True,
+                       timeout=300, cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert r.returncode == 0 and "replayed" in r.stdout, r.stdout + r.stderr
