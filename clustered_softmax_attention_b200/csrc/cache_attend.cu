@@ -163,17 +163,25 @@ struct Hide {
   __device__ __forceinline__ bool at(int nb, int t, int e) const { return edge && t >= left[nb][e]; }
 };
 
-// O += (p vstep) code with float16 weights; ds: the steps as float16 in the accumulators' unit,
-// in [2^-7, 2), two groups a register.
+// O += (p vstep) code; ds: the steps as float16 in the accumulators' unit, in [2^-7, 2), two groups
+// a register.  p vstep is the sum of two float16: the rounded product of p's upper piece, and what that
+// rounding cut off together with p's lower piece: 21 bits, and never coarser than 2^-23 of the unit, where
+// a weight at the reference is 2^9.  In one piece (11 bits, rounded twice) results differed from float32
+// arithmetic's by a bfloat16 step in one element of thirty (1e-3 in norm, 5e-5 in two pieces).  8 x 8
+// heads of 32768 tokens, 128 + 128 channels, one piece and two: 8 rows 88 and 96 us, 64 rows 363 and 452.
 template <int Dv, int NB>
 __device__ __forceinline__ void values_f16(Acc<Dv, NB> &acc, const uint8_t *codes,
                                            const uint32_t (&ds)[4][Dv / 64], const Tok<NB> &tk,
                                            int lane) {
-  __half2 p[NB][4];
+  __half2 p[NB][4], rest[NB][4];
 #pragma unroll
   for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) p[nb][i] = __floats2half2_rn(tk.p[nb][i][0], tk.p[nb][i][1]);
+    for (int i = 0; i < 4; ++i) {
+      p[nb][i] = __floats2half2_rn(tk.p[nb][i][0], tk.p[nb][i][1]);
+      rest[nb][i] = __floats2half2_rn(tk.p[nb][i][0] - __low2float(p[nb][i]),
+                                      tk.p[nb][i][1] - __high2float(p[nb][i]));
+    }
 #pragma unroll
   for (int kk = 0; kk < 2; ++kk) {
     uint32_t x[2][Dv / 32];
@@ -195,18 +203,27 @@ __device__ __forceinline__ void values_f16(Acc<Dv, NB> &acc, const uint8_t *code
       }
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
-        const uint32_t b0 = turned(bits(__hmul2(p[nb][2 * kk], f[0])));
-        const uint32_t b1 = turned(bits(__hmul2(p[nb][2 * kk + 1], f[1])));
-        mma_f16(acc.o[nb][2 * grp], a0, b0, b1);
-        mma_f16(acc.o[nb][2 * grp + 1], a1, b0, b1);
+        uint32_t hi[2], lo[2];
+#pragma unroll
+        for (int ii = 0; ii < 2; ++ii) {
+          const int i = 2 * kk + ii;
+          const __half2 w = __hmul2(p[nb][i], f[ii]);
+          // what the product's rounding cut off (exact), and the rest of the weight
+          lo[ii] = turned(bits(__hfma2(rest[nb][i], f[ii], __hfma2(p[nb][i], f[ii], __hneg2(w)))));
+          hi[ii] = turned(bits(w));
+        }
+        mma_f16(acc.o[nb][2 * grp], a0, hi[0], hi[1]);
+        mma_f16(acc.o[nb][2 * grp + 1], a1, hi[0], hi[1]);
+        mma_f16(acc.o[nb][2 * grp], a0, lo[0], lo[1]);
+        mma_f16(acc.o[nb][2 * grp + 1], a1, lo[0], lo[1]);
       }
     }
   }
 }
 
-// The same with p vstep in PARTS bfloat16 pieces (16 or 24 bits): any range.  The sum over the
-// tile's 32 tokens is formed apart and added once.
-template <int Dv, int NB, int PARTS>
+// The same with p vstep in three bfloat16 pieces (24 bits): any range.  The sum over the tile's 32
+// tokens is formed apart and added once.
+template <int Dv, int NB>
 __device__ __forceinline__ void values_wide(Acc<Dv, NB> &acc, const uint8_t *codes,
                                             const uint8_t *vstep, const Tok<NB> &tk,
                                             const float (&unit)[Dv / 32], const Hide<NB> &hide,
@@ -244,7 +261,7 @@ __device__ __forceinline__ void values_wide(Acc<Dv, NB> &acc, const uint8_t *cod
             w[ii][e] = hide.at(nb, 8 * i + g, e) ? 0.f : tk.p[nb][i][e] * f[ii];
           }
 #pragma unroll
-        for (int part = 0; part < PARTS; ++part) {
+        for (int part = 0; part < 3; ++part) {
           uint32_t b[2];
 #pragma unroll
           for (int ii = 0; ii < 2; ++ii) {
@@ -623,12 +640,12 @@ attend(const __grid_constant__ AttendArgs a, const __grid_constant__ CacheView v
         }
       }
       if (sizeof(T) == 4) {
-        values_wide<Dv, NB, 3>(acc, tile + S::kV, tile + S::kVStep, tk, unit, hide, lane);
+        values_wide<Dv, NB>(acc, tile + S::kV, tile + S::kVStep, tk, unit, hide, lane);
       } else {
         // A step in [2^-7, 2) of the unit (exponent field 8..15 of a float16; with bfloat16's 7
-        // bits below it, so one shift is left) is exact, p at most 2^14, and their product a
-        // float16 of 11 bits from p = 2^-7 on, 2^-16 of the reference.  A tile with another step
-        // (a jump of the values' size, a zero, a NaN) goes the wide way.
+        // bits below it, so one shift is left) is exact, p at most 2^14, and their product below
+        // 2^15.  A tile with another step (a jump of the values' size, a zero, a NaN) goes the wide
+        // way.
         uint32_t off_range = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -639,7 +656,7 @@ attend(const __grid_constant__ AttendArgs a, const __grid_constant__ CacheView v
             ds[i][w] <<= 3;
           }
         if (__builtin_expect(__any_sync(kAll, off_range & 0xfc00fc00u), 0))
-          values_wide<Dv, NB, 2>(acc, tile + S::kV, tile + S::kVStep, tk, unit, hide, lane);
+          values_wide<Dv, NB>(acc, tile + S::kV, tile + S::kVStep, tk, unit, hide, lane);
         else
           values_f16<Dv, NB>(acc, tile + S::kV, ds, tk, lane);
       }

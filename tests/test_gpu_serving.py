@@ -745,3 +745,35 @@ def test_the_first_calls_of_a_process_are_captured(H, M):
     r = subprocess.run([sys.executable, "-c", FIRST_CALL.format(H=H, M=M)], capture_output=True, text=True,
                        timeout=300, cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
     assert r.returncode == 0 and "replayed" in r.stdout, r.stdout + r.stderr
+
+
+def fine_close(got, Q, s, lens, counts, scale):
+    """bfloat16 rows whose weights are not rounded to fewer bits than float32 arithmetic needs: as
+    attend_close, but a weight is off by 2^-20 (two float16 pieces: the upper product's rounding is
+    kept, the lower piece, at most 2^-10 of it, is rounded to 2^-21, and the weight's own lower piece to
+    2^-22), or by 2^-23 in the unit where some step is 2^-3 and the normaliser 2^9: 2^-29 of the largest
+    value.  Weights of 11 bits (2^-11, twice) would fail wherever a row's values cancel: a sum of T
+    values of either sign is off by 2^-12 A / sqrt(T), more than all of this for short T."""
+    K, V = s.values()
+    ref, _, A, X = so.cache_attend(host(Q), K, V, lens, counts, scale)
+    for b in range(Q.shape[0]):
+        c, T = counts[b], lens[b]
+        big = np.abs(V[b][:, :T]).max() * T * 2.0 ** -29
+        e = (42 * U * X[b, :, :c] + 4 * U)[..., None]
+        tol = HALF[BF16] * np.abs(ref[b, :, :c]) + A[b, :, :c] * (2 * e + 2.0 ** -20 + 2 * U * (T / 16 + 40)) + big
+        d = np.abs(got[b, :, :c] - ref[b, :, :c])
+        assert (d <= tol).all(), (b, int((d > tol).sum()), float((d / tol).max()))
+
+
+FINE = [(8, 8, 1), (16, 2, 1), (16, 2, 2), (16, 2, 4), (16, 2, 8)]   # 1, 8, 16, 32, 64 rows
+
+
+@pytest.mark.parametrize("D,Dv", WIDTHS)
+@pytest.mark.parametrize("H,Hkv,M", FINE)
+def test_weights_of_bfloat16_rows_keep_their_bits(H, Hkv, M, D, Dv):
+    lens = [32, 70, 200]
+    s = filled(3, Hkv, 32, 8, D, Dv, 200)
+    Q = randn(11, 3, H, M, D, dtype=BF16)
+    out, _ = m.muse_cache_attend(Q, s.cache, s.table, ints(lens), scale=0.02)
+    fine_close(host(out), Q, s, lens, [M] * 3, 0.02)
+    ok()
