@@ -177,6 +177,7 @@ attend_tc(const __grid_constant__ AttendArgs a, const __grid_constant__ CacheVie
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 0) {
+    __syncwarp();  // lane 0 has set up the barriers
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      saddr(&sm.tmem_base)),
                  "r"(kTmemCols)
@@ -603,6 +604,7 @@ attend_tc(const __grid_constant__ AttendArgs a, const __grid_constant__ CacheVie
 #pragma unroll 1
         for (int c0 = 0; c0 < Dv; c0 += 64) {
           float y[64];
+          __syncwarp();  // lanes without a row have not stored: the loads below take the whole warp
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             float o[16];

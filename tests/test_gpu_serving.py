@@ -777,3 +777,16 @@ def test_weights_of_bfloat16_rows_keep_their_bits(H, Hkv, M, D, Dv):
     out, _ = m.muse_cache_attend(Q, s.cache, s.table, ints(lens), scale=0.02)
     fine_close(host(out), Q, s, lens, [M] * 3, 0.02)
     ok()
+
+
+@pytest.mark.parametrize("D,Dv", [(64, 128), (128, 128)])
+@pytest.mark.parametrize("H,M,counts", [(1, 66, [66, 65]), (4, 33, [17, 33]), (3, 128, [127, 23])])
+def test_many_rows_in_warps_that_are_partly_filled(H, M, counts, D, Dv):
+    """Two blocks of 64 value channels, rows that end inside a warp, items whole and split: lanes
+    without a row take part in every load of the accumulators."""
+    s = filled(2, 1, 64, 40, D, Dv, 2500)
+    Q = randn(12, 2, H, M, D, dtype=BF16)
+    for lens in ([2500, 1900], [200, 64]):
+        out, lse = m.muse_cache_attend(Q, s.cache, s.table, ints(lens), ints(counts), scale=0.1)
+        attend_close(host(out), host(lse), Q, s, lens, counts, 0.1, BF16)
+    ok()
