@@ -167,6 +167,7 @@ coef_tc(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ MuseT
   constexpr uint32_t kCols = OUT ? (CK > 128 ? 512u : 256u) : (uint32_t)CK;
   constexpr uint32_t kO = CK, kP = CK + OV;
   if (warp == 0) {
+    __syncwarp();  // lane 0 has set up the barriers
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      saddr(&sm.tmem_base)),
                  "r"(kCols)

@@ -228,6 +228,7 @@ km_assign_tc(const __grid_constant__ CUtensorMap map0, const __grid_constant__ C
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 0) {
+    __syncwarp();  // lane 0 has set up the barriers
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      saddr(&sm.tmem_base)),
                  "r"(256)
