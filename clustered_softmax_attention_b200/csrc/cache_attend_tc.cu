@@ -5,7 +5,7 @@
 // for 128 rows into shared memory instead of into every warp's registers.  Per tile of 128 tokens:
 //   producers (8 warps)  codes -> float16 K' and V' in 128-byte swizzled shared memory, two stages;
 //   issuer               S = Q K'^T into TMEM (two buffers), O += P V' with P from TMEM;
-//   softmax (4 warps)    a row a thread: S from TMEM, weights to TMEM, O in TMEM moved only
+//   softmax (4 warps)    a row a thread: S from TMEM, weights over it, O in TMEM moved only
 //                        when the running reference moves.
 // S of the next tile is issued before O += P V' of this one, so the softmax of one tile runs
 // beside both products.
@@ -39,7 +39,12 @@ constexpr int kTok = 128;               // tokens of a tile
 constexpr int kSoftmaxWarps = 4, kProducers = 8, kIssuer = kSoftmaxWarps + kProducers;
 constexpr int kThreads = 32 * (kIssuer + 1);
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kS = 0, kO = 256, kP = 384;  // TMEM columns: S (two of 128), O, P (two of 64)
+// TMEM columns: S (two of 128), O.  A weight takes the place of its S as two float16 pieces, 21 bits:
+// sixteen tokens' columns hold eight of upper and eight of lower pieces.  In one piece (11 bits) results
+// differed from float32 arithmetic's by 9e-4 in norm, in two by 1.6e-4.  One piece and two, 128 + 128
+// channels: 2 x 2 heads of 16384 tokens, 512 rows a head, 55 and 63 us; 8 x 8 heads, 68 rows, 170 and 204
+// (the second products take about 12 of the 34, the pieces and their stores the rest).
+constexpr uint32_t kS = 0, kO = 256;
 
 template <int D, int Dv>
 struct __align__(1024) Smem {
@@ -88,6 +93,14 @@ __device__ __forceinline__ void arrived(uint32_t (&x)[16]) {
                  "+r"(x[13]), "+r"(x[14]), "+r"(x[15])
                :
                : "memory");
+}
+__device__ __forceinline__ __half2 halves(uint32_t x) { return *reinterpret_cast<const __half2 *>(&x); }
+// x and y as two float16 each, 21 bits: the upper pieces (cut to 11 bits) packed, the lower ones packed.
+__device__ __forceinline__ void split_f16(float x, float y, uint32_t &hi, uint32_t &lo) {
+  const float a = __uint_as_float(__float_as_uint(x) & 0xffffe000u);
+  const float b = __uint_as_float(__float_as_uint(y) & 0xffffe000u);
+  hi = pack_f16(a, b);
+  lo = pack_f16(x - a, y - b);
 }
 // The 16-byte chunk c of a 128-byte row.
 __device__ __forceinline__ uint4 *chunk(__half *block, int row, int c) {
@@ -418,9 +431,12 @@ attend_tc(const __grid_constant__ AttendArgs a, const __grid_constant__ CacheVie
         tc_fence_after();
         if (lane == 0) {
           constexpr uint32_t id = idesc_f16(kTcRows, Dv) | (1u << 16);
-          for (int kk = 0; kk < kTok / 16; ++kk)
-            tc_mma_ts(tmem + kO, tmem + kP + (u & 1) * 64 + kk * 8, sdesc_mn(sm.v[u & 1][0] + kk * 16 * 64),
-                      id, u > it0 || kk > 0 ? 1u : 0u);
+          for (int kk = 0; kk < kTok / 16; ++kk) {
+            const uint32_t p = tmem + kS + (u & 1) * 128 + kk * 16;
+            const uint64_t rows = sdesc_mn(sm.v[u & 1][0] + kk * 16 * 64);
+            tc_mma_ts(tmem + kO, p, rows, id, u > it0 || kk > 0 ? 1u : 0u);
+            tc_mma_ts(tmem + kO, p + 8, rows, id, 1u);
+          }
           tc_commit(&sm.kv_empty[u & 1]);
         }
         __syncwarp();
@@ -505,74 +521,20 @@ attend_tc(const __grid_constant__ AttendArgs a, const __grid_constant__ CacheVie
 #pragma unroll
         for (int k = 0; k < kProducers; ++k) gone |= sm.gone[st][k] << k;
         const bool edge = see_all - t * kTok < kTok || gone;
-        // weights are 2^9 at the reference, which moves when one would pass 2^14: they are formed
-        // with the reference as it is, and, where it has to move (the first tile, a few more),
-        // once again
-        float sum;
-        for (int again = 0;; ++again) {
-          float top = -CUDART_INF_F;
-          sum = 0.f;
-          const float ref = mx == -CUDART_INF_F ? 0.f : mx;
-          float sums[2] = {0.f, 0.f};
-          // sixteen columns: c's weights from x
-          auto some = [&](int c, const uint32_t (&x)[16], bool masked) {
-            float y[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              y[e] = __uint_as_float(x[e]);
-              if (masked && (16 * c + e >= left || (gone >> c) & 1)) y[e] = -CUDART_INF_F;
-            }
-            const float to2 = fmaxf(sm.scale[st][c] * rf, 1e-37f);  // to logits in units of log 2
-            float m0 = fmaxf(y[0], y[1]), m1 = fmaxf(y[2], y[3]);
-#pragma unroll
-            for (int e = 4; e < 16; e += 4) {
-              m0 = fmaxf(m0, fmaxf(y[e], y[e + 1]));
-              m1 = fmaxf(m1, fmaxf(y[e + 2], y[e + 3]));
-            }
-            top = fmaxf(top, fmaxf(m0, m1) * to2);
-            uint32_t pk[8];
-#pragma unroll
-            for (int e = 0; e < 16; e += 2) {
-              const float p0 = ex2(fmaf(y[e], to2, -ref)), p1 = ex2(fmaf(y[e + 1], to2, -ref));
-              sums[(e >> 1) & 1] += p0 + p1;
-              pk[e >> 1] = pack_f16(p0, p1);
-            }
-            tmem_st8(tmem + lane_base + kP + st * 64 + c * 8, pk);
-          };
-          if (__builtin_expect(edge, 0)) {
-#pragma unroll 1
-            for (int c = 0; c < 8; ++c) {
-              uint32_t x[16];
-              tmem_ld16_async(col + c * 16, x);
-              arrived(x);
-              some(c, x, true);
-            }
-          } else {
-            uint32_t x[4][16];
-            tmem_ld16_async(col, x[0]);
-            tmem_ld16_async(col + 16, x[1]);
-#pragma unroll
-            for (int c = 0; c < 8; c += 2) {
-              const int k = c & 2;
-              arrived(x[k]);
-              arrived(x[k + 1]);
-              if (c < 6) {
-                tmem_ld16_async(col + (c + 2) * 16, x[k ^ 2]);
-                tmem_ld16_async(col + (c + 3) * 16, x[(k ^ 2) + 1]);
-              }
-              some(c, x[k], false);
-              some(c + 1, x[k + 1], false);
-            }
-          }
-          sum = sums[0] + sums[1];
-          tmem_st_wait();
-          if (again || __builtin_expect(!__any_sync(kAll, top > mx + 14.f), 1)) break;
+        // to logits in units of log 2
+        auto to2 = [&](int c) { return fmaxf(sm.scale[st][c] * rf, 1e-37f); };
+        float sums[2] = {0.f, 0.f};
+        // The reference moves: what was summed and weighed by it, the tile's first `done` chunks of
+        // weights among them, is brought to the new one.
+        auto move = [&](float top, int done) {
           const float now = fmaxf(mx, top - 9.f);
           const float fix = now == -CUDART_INF_F ? 1.f : ex2(mx - now);
           mx = now;
           l *= fix;
+          sums[0] *= fix;
+          sums[1] *= fix;
           if (it > it0) {
-            if (!wait(&sm.kv_empty[(it - 1) & 1], (it - 1) >> 1)) break;  // O holds all tiles so far
+            if (!wait(&sm.kv_empty[(it - 1) & 1], (it - 1) >> 1)) return;  // O holds all tiles so far
             tc_fence_after();
 #pragma unroll 1
             for (int c = 0; c < Dv / 16; ++c) {
@@ -584,11 +546,92 @@ attend_tc(const __grid_constant__ AttendArgs a, const __grid_constant__ CacheVie
               tmem_st8(tmem + lane_base + kO + c * 16, w[0]);
               tmem_st8(tmem + lane_base + kO + c * 16 + 8, w[1]);
             }
-            tmem_st_wait();
+          }
+          tmem_st_wait();
+#pragma unroll 1
+          for (int c = 0; c < done; ++c) {
+            float o[16];
+            uint32_t hi[8], lo[8];
+            tmem_ld16(col + c * 16, o);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float2 u = __half22float2(halves(__float_as_uint(o[e])));
+              const float2 v = __half22float2(halves(__float_as_uint(o[8 + e])));
+              split_f16((u.x + v.x) * fix, (u.y + v.y) * fix, hi[e], lo[e]);
+            }
+            tmem_st8(col + c * 16, hi);
+            tmem_st8(col + c * 16 + 8, lo);
+          }
+        };
+        // The largest logit of two chunks of sixteen columns.  Weights are 2^9 at the reference, which
+        // moves when one would pass 2^14 (in the first tile, a few more).
+        auto top_of = [&](int c, const uint32_t (&x)[2][16]) {
+          float top = -CUDART_INF_F;
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            float m[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              m[e] = fmaxf(fmaxf(__uint_as_float(x[k][e]), __uint_as_float(x[k][e + 4])),
+                           fmaxf(__uint_as_float(x[k][e + 8]), __uint_as_float(x[k][e + 12])));
+            top = fmaxf(top, fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])) * to2(c + k));
+          }
+          return top;
+        };
+        auto weigh = [&](int c, const uint32_t (&x)[2][16]) {
+          const float ref = mx == -CUDART_INF_F ? 0.f : mx;
+          uint32_t w[32];  // the two chunks' upper and lower pieces
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const float f = to2(c + k);
+#pragma unroll
+            for (int e = 0; e < 16; e += 2) {
+              const float p0 = ex2(fmaf(__uint_as_float(x[k][e]), f, -ref));
+              const float p1 = ex2(fmaf(__uint_as_float(x[k][e + 1]), f, -ref));
+              sums[(e >> 1) & 1] += p0 + p1;
+              split_f16(p0, p1, w[16 * k + (e >> 1)], w[16 * k + 8 + (e >> 1)]);
+            }
+          }
+          tmem_st32(col + c * 16, w);
+        };
+        if (__builtin_expect(edge, 0)) {
+#pragma unroll 1
+          for (int c = 0; c < 8; c += 2) {
+            uint32_t x[2][16];
+            tmem_ld16_async(col + c * 16, x[0]);
+            tmem_ld16_async(col + c * 16 + 16, x[1]);
+            arrived(x[0]);
+            arrived(x[1]);
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+              for (int e = 0; e < 16; ++e)
+                if (16 * (c + k) + e >= left || (gone >> (c + k)) & 1) x[k][e] = 0xff800000u;  // -infinity
+            const float top = top_of(c, x);
+            if (__any_sync(kAll, top > mx + 14.f)) move(top, c);
+            weigh(c, x);
+          }
+        } else {
+          uint32_t x[2][2][16];
+          tmem_ld16_async(col, x[0][0]);
+          tmem_ld16_async(col + 16, x[0][1]);
+#pragma unroll
+          for (int c = 0; c < 8; c += 2) {
+            const int k = (c >> 1) & 1;
+            arrived(x[k][0]);
+            arrived(x[k][1]);
+            const float top = top_of(c, x[k]);
+            if (__builtin_expect(__any_sync(kAll, top > mx + 14.f), 0)) move(top, c);
+            if (c < 6) {
+              tmem_ld16_async(col + (c + 2) * 16, x[k ^ 1][0]);
+              tmem_ld16_async(col + (c + 3) * 16, x[k ^ 1][1]);
+            }
+            weigh(c, x[k]);
           }
         }
         if (!ok) break;
-        l += sum;
+        tmem_st_wait();
+        l += sums[0] + sums[1];
         tc_fence_before();
         mbar_arrive(&sm.p_full[st]);
       }

@@ -765,7 +765,8 @@ def fine_close(got, Q, s, lens, counts, scale):
         assert (d <= tol).all(), (b, int((d > tol).sum()), float((d / tol).max()))
 
 
-FINE = [(8, 8, 1), (16, 2, 1), (16, 2, 2), (16, 2, 4), (16, 2, 8)]   # 1, 8, 16, 32, 64 rows
+FINE = [(8, 8, 1), (16, 2, 1), (16, 2, 2), (16, 2, 4), (16, 2, 8),   # 1, 8, 16, 32, 64 rows
+        (4, 2, 40), (8, 2, 64)]                                        # 80, 256: the other form
 
 
 @pytest.mark.parametrize("D,Dv", WIDTHS)
