@@ -318,9 +318,11 @@ attend_tc(const __grid_constant__ AttendArgs a, const __grid_constant__ CacheVie
             vs[i][1][0] = y.y;
           }
           // fields 12..27 of keys, 8..23 of values (18: the first tile's largest); n < 16 also goes
-          // the careful way, for the tokens that are not there
+          // the careful way, for the tokens that are not there.  k_shift is above zero where the largest
+          // is tiny, and a NaN (0xffff) comes back into range with it: its sign tells.
 #pragma unroll
-          for (int w = 0; w < NGk / 2; ++w) off_range |= ks[i][w] + k_shift - 0x06000600u;
+          for (int w = 0; w < NGk / 2; ++w)
+            off_range |= (ks[i][w] + k_shift - 0x06000600u) | (ks[i][w] & 0x80008000u);
 #pragma unroll
           for (int w = 0; w < Dv / 64; ++w)
             off_range |= (vs[i][0][w] + shift[w] - 0x04000400u) | (vs[i][1][w] + shift[w] - 0x04000400u);

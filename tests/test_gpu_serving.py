@@ -791,3 +791,29 @@ def test_many_rows_in_warps_that_are_partly_filled(H, M, counts, D, Dv):
         out, lse = m.muse_cache_attend(Q, s.cache, s.table, ints(lens), ints(counts), scale=0.1)
         attend_close(host(out), host(lse), Q, s, lens, counts, 0.1, BF16)
     ok()
+
+
+@pytest.mark.parametrize("D,Dv", WIDTHS)
+@pytest.mark.parametrize("what", ["nan", "inf", "zeros and a nan low", "zeros and a nan high", "tiny and a nan"])
+@pytest.mark.parametrize("H,M", [(2, 4), (2, 40), (8, 16)])
+def test_keys_that_are_all_nan_or_zero_but_for_one(H, M, what, D, Dv):
+    """Sixteen neighbouring tokens whose only steps are NaN, zero or tiny: rows that see a NaN are NaN,
+    and no others."""
+    T, at = 256, 160
+    s = Store(1, 1, 64, 4, D, Dv)
+    K, V = randn(1, 1, 1, T, D), randn(2, 1, 1, T, Dv)
+    first, last = at + 5, at + 5          # tokens that hold a NaN
+    if what in ("nan", "inf"):
+        K[0, 0, at:at + 16] = float(what)
+        first, last = at, at + 15
+    else:
+        K[0, 0, at:at + 16] *= 1e-36 if "tiny" in what else 0
+        K[0, 0, first, 40 if "high" in what else 3] = float("nan")
+    m.muse_cache_write(s.cache, K, V, s.table, ints([0]))
+    Q = randn(3, 1, H, M, D, dtype=BF16)
+    for length in (T, at + 8, at + 5 + M // 2, at):
+        out, lse = m.muse_cache_attend(Q, s.cache, s.table, ints([length]), scale=0.1)
+        sees = torch.arange(length - M, length).cuda() >= first
+        assert torch.equal(torch.isnan(out).all(-1), sees.expand(1, H, M)), length
+        assert torch.equal(torch.isnan(lse), sees.expand(1, H, M)) and torch.isfinite(out[:, :, ~sees]).all()
+    ok()
