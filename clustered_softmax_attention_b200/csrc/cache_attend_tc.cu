@@ -11,8 +11,8 @@
 // beside both products.
 //   K' = code step 2^(12 - e), e the exponent of the largest step of sixteen tokens: exact for
 //   steps down to 2^-26 of that, off by 2^-37 of it below; 2^(e - 12) multiplies their columns of S.
-//   V' = code step unit[group], a power of two that the span's first tile sets; exact for steps
-//   from 2^-10 to 2^5 of its largest, and, zero steps apart, a tile with others makes the span go
+//   V' = code step unit[group], a power of two that the group's first tile of the span that is not all
+//   zeros sets; exact for steps from 2^-10 to 2^5 of its largest, and, zero steps apart, a tile with others makes the span go
 //   the slow way: its rows are computed again in float32 from the codes.
 // The order of channels inside K' and V' is the one in which a word's codes come out, two nibbles
 // four apart a register; Q is laid out alike, and the output's columns are put back at the end.
@@ -55,7 +55,7 @@ struct __align__(1024) Smem {
   uint8_t raw[kProducers][2][9 * (D + Dv)];
   float scale[2][kProducers]; // what sixteen tokens' columns of S are multiplied by
   float unit[4][Dv / 32];     // by span
-  uint32_t big[2][kProducers][Dv / 64];  // by span
+  uint32_t big[2][kProducers][Dv / 64];  // by exchange
   int exps[kTcRows];          // of the queries' powers of two
   float slow_q[kSoftmaxWarps][D];
   int bad[4];                 // number (from 1) of the last span that has to go the slow way
@@ -215,6 +215,8 @@ attend_tc(const __grid_constant__ AttendArgs a, const __grid_constant__ CacheVie
     const int pw = warp - kSoftmaxWarps;  // tokens 16 pw .. 16 pw + 15 of a tile
     constexpr int kRV = 8 * D, kRKS = 8 * (D + Dv), kRVS = kRKS + D;
     uint32_t shift[Dv / 64];
+    uint32_t open = 0;       // groups that have no unit yet, in every producer alike
+    uint32_t exchanges = 0;
     // the tile after the one at hand is under way: raw[it & 1] holds tile it
     bool next_here = false;
     auto fetch = [&](const Span &s, int t, uint32_t slot) {
@@ -256,7 +258,14 @@ attend_tc(const __grid_constant__ AttendArgs a, const __grid_constant__ CacheVie
         const uint8_t *raw = sm.raw[pw][st];
         const int n = here ? min(16, cur.len - base) : 0;  // its tokens
         if (t == cur.t0) {
-          // the values' unit: the span's first tile's largest step comes to [2^3, 2^4)
+          open = (1u << NG) - 1;
+#pragma unroll
+          for (int w = 0; w < Dv / 64; ++w) shift[w] = 0;
+          if (pw == 0 && lane < NG) sm.unit[span & 3][lane] = 1.f;
+        }
+        if (open) {
+          // The values' unit: the largest step of the group's first tile that has one comes to
+          // [2^3, 2^4).  Before that the group adds nothing to O, and any unit is right.
           uint32_t big[Dv / 64];
 #pragma unroll
           for (int w = 0; w < Dv / 64; ++w) {
@@ -264,23 +273,26 @@ attend_tc(const __grid_constant__ AttendArgs a, const __grid_constant__ CacheVie
             big[w] = lane < n ? __vmaxs2(0u, reinterpret_cast<const uint32_t *>(raw + kRVS)[lane * (Dv / 64) + w]) : 0u;
 #pragma unroll
             for (int o = 16; o; o >>= 1) big[w] = __vmaxs2(big[w], __shfl_xor_sync(kAll, big[w], o));
-            if (lane == 0) sm.big[span & 1][pw][w] = big[w];
+            if (lane == 0) sm.big[exchanges & 1][pw][w] = big[w];
           }
           mbar_arrive(&sm.unit_full);
-          if (!wait(&sm.unit_full, span - 1)) break;
+          if (!wait(&sm.unit_full, exchanges)) break;
 #pragma unroll
           for (int w = 0; w < Dv / 64; ++w) {
 #pragma unroll
-            for (int k = 0; k < kProducers; ++k) big[w] = __vmaxs2(big[w], sm.big[span & 1][k][w]);
-            shift[w] = 0;
+            for (int k = 0; k < kProducers; ++k) big[w] = __vmaxs2(big[w], sm.big[exchanges & 1][k][w]);
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-              const int ex = min(max((int)((big[w] >> (16 * k + 7)) & 255u) - 127, -40), 60);
+              const uint32_t step = (big[w] >> (16 * k)) & 0xffffu;
+              if (!step || !((open >> (2 * w + k)) & 1)) continue;
+              open &= ~(1u << (2 * w + k));
+              const int ex = min(max((int)(step >> 7) - 127, -40), 60);
               // float16's exponent is 112 less than bfloat16's
               shift[w] += (uint32_t)((3 - ex - 112) * 128) << (16 * k);
               if (pw == 0 && lane == 0) sm.unit[span & 3][2 * w + k] = ldexpf(1.f, 3 - ex);
             }
           }
+          ++exchanges;
         }
         if (it >= 2 && !wait(&sm.kv_empty[st], (it - 2) >> 1)) break;
         if (lane == 0) sm.gone[st][pw] = !here && base < cur.len;

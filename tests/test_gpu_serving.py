@@ -817,3 +817,41 @@ def test_keys_that_are_all_nan_or_zero_but_for_one(H, M, what, D, Dv):
         assert torch.equal(torch.isnan(out).all(-1), sees.expand(1, H, M)), length
         assert torch.equal(torch.isnan(lse), sees.expand(1, H, M)) and torch.isfinite(out[:, :, ~sees]).all()
     ok()
+
+
+def duration(f):
+    """Shortest of some calls, ms."""
+    f()
+    times = []
+    for _ in range(5):
+        a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        a.record()
+        f()
+        b.record()
+        b.synchronize()
+        times.append(a.elapsed_time(b))
+    return min(times)
+
+
+@pytest.mark.parametrize("D,Dv", WIDTHS)
+@pytest.mark.parametrize("H,M", [(16, 4), (32, 40)])
+def test_values_that_begin_with_zeros(H, M, D, Dv):
+    """Some groups zero over the first tokens, over all tokens, or over none: the answer, and about
+    the time, of ordinary values (the next tile's size is what counts, not the first one's)."""
+    B, Hkv, T = 2, 16, 2000
+    s = Store(B, Hkv, 64, 32, D, Dv)
+    K, V = randn(1, B, Hkv, T, D), randn(2, B, Hkv, T, Dv)
+    Q = randn(3, B, H, M, D, dtype=BF16)
+    call = lambda: m.muse_cache_attend(Q, s.cache, s.table, ints([T, T - 77]), scale=0.1)
+    m.muse_cache_write(s.cache, K, V, s.table, ints([0] * B))
+    plain = duration(call)
+    V[0, :, :300] = 0
+    V[1, :, :1100, :32] = 0
+    V[1, ..., Dv - 32:] = 0
+    m.muse_cache_write(s.cache, K, V, s.table, ints([0] * B))
+    out, lse = call()
+    attend_close(host(out), host(lse), Q, s, [T, T - 77], [M] * B, 0.1, BF16)
+    assert (out[1, ..., Dv - 32:] == 0).all()
+    # (recomputing a stretch on the CUDA cores took a hundred times as long)
+    assert duration(call) < 5 * plain + 0.05
+    ok()
