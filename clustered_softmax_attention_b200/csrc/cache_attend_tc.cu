@@ -12,8 +12,9 @@
 //   K' = code step 2^(12 - e), e the exponent of the largest step of sixteen tokens: exact for
 //   steps down to 2^-26 of that, off by 2^-37 of it below; 2^(e - 12) multiplies their columns of S.
 //   V' = code step unit[group], a power of two that the group's first tile of the span that is not all
-//   zeros sets; exact for steps from 2^-10 to 2^5 of its largest, and, zero steps apart, a tile with others makes the span go
-//   the slow way: its rows are computed again in float32 from the codes.
+//   zeros sets by its usual largest step: exact for steps from 2^-17 to 2^9 of that.  Sixteen tokens with
+//   a step outside of it (zero apart) have V' = 0, and the softmax warps add p v to O in float32 from
+//   the codes.
 // The order of channels inside K' and V' is the one in which a word's codes come out, two nibbles
 // four apart a register; Q is laid out alike, and the output's columns are put back at the end.
 //
@@ -39,6 +40,8 @@ constexpr int kTok = 128;               // tokens of a tile
 constexpr int kSoftmaxWarps = 4, kProducers = 8, kIssuer = kSoftmaxWarps + kProducers;
 constexpr int kThreads = 32 * (kIssuer + 1);
 constexpr uint32_t kTmemCols = 512;
+constexpr int kGone = 1;    // not in the cache
+constexpr int kValues = 2;  // value steps that V' does not hold: it holds zeros
 // TMEM columns: S (two of 128), O.  A weight takes the place of its S as two float16 pieces, 21 bits:
 // sixteen tokens' columns hold eight of upper and eight of lower pieces.  In one piece (11 bits) results
 // differed from float32 arithmetic's by 9e-4 in norm, in two by 1.6e-4.  One piece and two, 128 + 128
@@ -55,11 +58,10 @@ struct __align__(1024) Smem {
   uint8_t raw[kProducers][2][9 * (D + Dv)];
   float scale[2][kProducers]; // what sixteen tokens' columns of S are multiplied by
   float unit[4][Dv / 32];     // by span
-  uint32_t big[2][kProducers][Dv / 64];  // by exchange
+  alignas(4) uint16_t big[2][kProducers][Dv / 32];  // by exchange
   int exps[kTcRows];          // of the queries' powers of two
-  float slow_q[kSoftmaxWarps][D];
-  int bad[4];                 // number (from 1) of the last span that has to go the slow way
-  int gone[2][kProducers];    // sixteen tokens that are not in the cache
+  float tokens[kSoftmaxWarps][16 * 16];  // sixteen tokens' values, sixteen columns of O at a time
+  alignas(8) uint8_t odd[2][kProducers];  // kGone, kValues: what holds of sixteen tokens
   int64_t run[kThreads + kThreads / 32];
   uint64_t q_full, unit_full, kv_full[2], kv_empty[2], s_full[2], p_full[2], end;
   uint32_t tmem_base;
@@ -111,48 +113,60 @@ __host__ __device__ constexpr int column_of(int c) {
   return 8 * (c % 8) + (c / 8 < 4 ? 2 * (c / 8) : 2 * (c / 8 - 4) + 1);
 }
 
-// One row over the 32-token tiles [lo, hi) of its item, in float32 from the codes: a lane a token
-// for the logits, a channel of every group for the values.
+// O += p v of sixteen tokens whose value steps V' does not hold, in float32 from the codes: a row a
+// thread.  `logits`: their columns of S; `left`: tokens of them that the row sees; `p`: their tile of 32
+// tokens, whose half `part` they are; begin: O holds nothing yet.  Small rather than fast (3 us): a cold
+// kernel waits for its instructions.
 template <int D, int Dv>
-__device__ __noinline__ void slow_row(const AttendArgs &a, const CacheView &v, int b, int hk, int see,
-                                      int lo, int hi, const float *q, float &mx, float &l,
-                                      float (&o)[Dv / 32]) {
+__device__ __noinline__ void exact_values(uint32_t logits, float to2, float ref, int left, const uint8_t *p,
+                                          int part, const float *unit, uint32_t o_at, float *tokens,
+                                          bool begin) {
   using S = TileShape<D, Dv>;
-  const int lane = threadIdx.x & 31;
-  mx = -CUDART_INF_F;
-  l = 0.f;
-  for (int g = 0; g < Dv / 32; ++g) o[g] = 0.f;
-  for (int tile = lo; tile < hi && tile * 32 < see; ++tile) {
-    const uint8_t *p = cache_tile(v, b, hk, tile, S::kBytes);
-    if (!p) continue;
-    const uint32_t *kw = (const uint32_t *)p, *vw = (const uint32_t *)(p + S::kV);
-    const uint16_t *ks = (const uint16_t *)(p + S::kKStep), *vs = (const uint16_t *)(p + S::kVStep);
-    float x = 0.f;
-    for (int w = 0; w < D / 32; ++w) {
-      float s = 0.f;
-      for (int c = 0; c < 4; ++c) {
-        const uint32_t u = kw[key_word<D>(lane, c, w)];
-        for (int n = 0; n < 8; ++n) s = fmaf(code_value(u, n), q[32 * w + 8 * c + n], s);
-      }
-      x = fmaf(s, step_value(ks[lane * (D / 32) + w]), x);
+  const int lane = threadIdx.x & 31, t0 = 16 * part + (lane >> 1);
+  const uint32_t *vw = reinterpret_cast<const uint32_t *>(p + S::kV);
+  const uint16_t *vs = reinterpret_cast<const uint16_t *>(p + S::kVStep) + t0 * (Dv / 32);
+#pragma unroll 1
+  for (int j = 0; j < Dv / 16; ++j) {
+    // a lane a token and one of its words: channels g + 8 (0..7) of 64, in the order of the columns
+    const uint32_t word = vw[value_word<Dv>(t0, 2 * (j & 3) + (lane & 1), j >> 2)];
+    const int grp = 2 * (j >> 2);
+    const float f[2] = {step_value(vs[grp]) * unit[grp], step_value(vs[grp + 1]) * unit[grp + 1]};
+    float y[8];
+#pragma unroll
+    for (int n = 0; n < 8; ++n) y[2 * (n & 3) + (n >> 2)] = code_value(word, n) * f[n >> 2];
+    __syncwarp();  // the last columns' values have been read
+    float4 *to = reinterpret_cast<float4 *>(tokens + (lane >> 1) * 16 + (lane & 1) * 8);
+    to[0] = make_float4(y[0], y[1], y[2], y[3]);
+    to[1] = make_float4(y[4], y[5], y[6], y[7]);
+    __syncwarp();
+    float o[16];
+    tmem_ld16(o_at + j * 16, o);
+    if (begin) {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) o[e] = 0.f;
     }
-    const bool live = tile * 32 + lane < see;
-    const float top = fmaxf(mx, warp_max(live ? x : -CUDART_INF_F));
-    const float ref = top == -CUDART_INF_F ? 0.f : top;
-    const float fix = ex2(mx - ref), e = live ? ex2(x - ref) : 0.f;
-    mx = top;
-    l = l * fix + warp_sum(e);
-    for (int g = 0; g < Dv / 32; ++g) o[g] *= fix;
-    const int n = min(32, see - tile * 32);
-    for (int t = 0; t < n; ++t) {
-      const float pt = __shfl_sync(0xffffffffu, e, t);
-      for (int g = 0; g < Dv / 32; ++g) {
-        const int c = 32 * g + lane;
-        const uint32_t u = vw[value_word<Dv>(t, c & 7, c >> 6)] >> (4 * ((c & 63) >> 3));
-        o[g] = fmaf(pt * step_value(vs[t * (Dv / 32) + g]), code_value(u, 0), o[g]);
+#pragma unroll 1
+    for (int t = 0; t < 16; ++t) {
+      const float w = ex2(fmaf(tmem_ld1(logits + t), to2, -ref));
+      if (t < left) {  // whatever others hold
+#pragma unroll
+        for (int e = 0; e < 16; e += 4) {
+          const float4 x = *reinterpret_cast<const float4 *>(tokens + t * 16 + e);
+          o[e] = fmaf(w, x.x, o[e]);
+          o[e + 1] = fmaf(w, x.y, o[e + 1]);
+          o[e + 2] = fmaf(w, x.z, o[e + 2]);
+          o[e + 3] = fmaf(w, x.w, o[e + 3]);
+        }
       }
+      __syncwarp();
     }
+    uint32_t u[2][8];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) u[e >> 3][e & 7] = __float_as_uint(o[e]);
+    tmem_st8(o_at + j * 16, u[0]);
+    tmem_st8(o_at + j * 16 + 8, u[1]);
   }
+  tmem_st_wait();
 }
 
 template <int D, int Dv>
@@ -185,7 +199,6 @@ attend_tc(const __grid_constant__ AttendArgs a, const __grid_constant__ CacheVie
       mbar_init(&sm.s_full[i], 1);
       mbar_init(&sm.p_full[i], 128);
     }
-    for (int i = 0; i < 4; ++i) sm.bad[i] = 0;
     sm.abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -264,38 +277,45 @@ attend_tc(const __grid_constant__ AttendArgs a, const __grid_constant__ CacheVie
           if (pw == 0 && lane < NG) sm.unit[span & 3][lane] = 1.f;
         }
         if (open) {
-          // The values' unit: the largest step of the group's first tile that has one comes to
-          // [2^3, 2^4).  Before that the group adds nothing to O, and any unit is right.
-          uint32_t big[Dv / 64];
+          // The values' unit: in the group's first tile that has a step above zero, the largest of each
+          // sixteen tokens, and of these the median, comes to [2^3, 2^4): neither a few large values nor
+          // a few small ones put the others out of range.  Before that tile the group adds nothing to
+          // O, and any unit is right.
 #pragma unroll
           for (int w = 0; w < Dv / 64; ++w) {
             // a lane a token; NaN is negative here, and left out
-            big[w] = lane < n ? __vmaxs2(0u, reinterpret_cast<const uint32_t *>(raw + kRVS)[lane * (Dv / 64) + w]) : 0u;
+            uint32_t top = lane < n ? __vmaxs2(0u, reinterpret_cast<const uint32_t *>(raw + kRVS)[lane * (Dv / 64) + w]) : 0u;
 #pragma unroll
-            for (int o = 16; o; o >>= 1) big[w] = __vmaxs2(big[w], __shfl_xor_sync(kAll, big[w], o));
-            if (lane == 0) sm.big[exchanges & 1][pw][w] = big[w];
+            for (int o = 8; o; o >>= 1) top = __vmaxs2(top, __shfl_xor_sync(kAll, top, o));
+            if (lane == 0) reinterpret_cast<uint32_t *>(sm.big[exchanges & 1][pw])[w] = top;
           }
           mbar_arrive(&sm.unit_full);
           if (!wait(&sm.unit_full, exchanges)) break;
+          // a lane a group and sixteen tokens: the place of its largest among those above zero
+          const uint32_t mine = lane < NG * kProducers ? sm.big[exchanges & 1][lane / NG][lane % NG] : 0u;
+          uint32_t many = 0, below = 0;
+#pragma unroll 1
+          for (int k = 0; k < kProducers; ++k) {
+            const uint32_t x = __shfl_sync(kAll, mine, k * NG + lane % NG);
+            many += x > 0;
+            below += x > 0 && (x < mine || (x == mine && k < lane / NG));
+          }
+          uint32_t median = mine > 0 && below == (many - 1) / 2 ? mine : 0u;
 #pragma unroll
-          for (int w = 0; w < Dv / 64; ++w) {
+          for (int o = NG; o < 32; o <<= 1) median = max(median, __shfl_xor_sync(kAll, median, o));
 #pragma unroll
-            for (int k = 0; k < kProducers; ++k) big[w] = __vmaxs2(big[w], sm.big[exchanges & 1][k][w]);
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const uint32_t step = (big[w] >> (16 * k)) & 0xffffu;
-              if (!step || !((open >> (2 * w + k)) & 1)) continue;
-              open &= ~(1u << (2 * w + k));
-              const int ex = min(max((int)(step >> 7) - 127, -40), 60);
-              // float16's exponent is 112 less than bfloat16's
-              shift[w] += (uint32_t)((3 - ex - 112) * 128) << (16 * k);
-              if (pw == 0 && lane == 0) sm.unit[span & 3][2 * w + k] = ldexpf(1.f, 3 - ex);
-            }
+          for (int grp = 0; grp < NG; ++grp) {
+            const uint32_t step = __shfl_sync(kAll, median, grp);
+            if (!step || !((open >> grp) & 1)) continue;
+            open &= ~(1u << grp);
+            const int ex = min(max((int)(step >> 7) - 127, -40), 60);
+            // float16's exponent is 112 less than bfloat16's
+            shift[grp >> 1] += (uint32_t)((3 - ex - 112) * 128) << (16 * (grp & 1));
+            if (pw == 0 && lane == 0) sm.unit[span & 3][grp] = ldexpf(1.f, 3 - ex);
           }
           ++exchanges;
         }
         if (it >= 2 && !wait(&sm.kv_empty[st], (it - 2) >> 1)) break;
-        if (lane == 0) sm.gone[st][pw] = !here && base < cur.len;
         // ---- steps as float16.  Keys: the sixteen tokens' largest (a NaN is left out: it makes its
         // token NaN) comes to exponent field 27; values: by the span's unit.
         uint32_t top = 0;
@@ -309,6 +329,7 @@ attend_tc(const __grid_constant__ AttendArgs a, const __grid_constant__ CacheVie
         if (lane == 0) sm.scale[st][pw] = ldexpf(1.f, e_top - 127 - 12);
         const uint32_t k_shift = (uint32_t)((27 - e_top) * 128) * 0x10001u;
         uint32_t ks[2][NGk / 2], vs[2][2][Dv / 64], off_range = 0;
+        int odd = !here && base < cur.len ? kGone : 0;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           if (D == 128) {
@@ -329,7 +350,7 @@ attend_tc(const __grid_constant__ AttendArgs a, const __grid_constant__ CacheVie
             vs[i][0][0] = y.x;
             vs[i][1][0] = y.y;
           }
-          // fields 12..27 of keys, 8..23 of values (18: the first tile's largest); n < 16 also goes
+          // fields 12..27 of keys, 8..23 of values (18: the first tile's usual largest); n < 16 also goes
           // the careful way, for the tokens that are not there.  k_shift is above zero where the largest
           // is tiny, and a NaN (0xffff) comes back into range with it: its sign tells.
 #pragma unroll
@@ -352,7 +373,7 @@ attend_tc(const __grid_constant__ AttendArgs a, const __grid_constant__ CacheVie
           }
         } else {
           // half by half: tokens that are not there and zero steps are zero; a key step too small is
-          // zero too, a NaN NaN; a value step that float16 does not hold sends the span the slow way
+          // zero too, a NaN NaN; with a value step that float16 does not hold all values are zero here
 #pragma unroll 1
           for (int i = 0; i < 2; ++i) {
             auto careful = [&](uint32_t x, uint32_t by, bool live, bool value) {
@@ -361,7 +382,7 @@ attend_tc(const __grid_constant__ AttendArgs a, const __grid_constant__ CacheVie
               for (int k = 0; k < 2; ++k) {
                 const int s = (int)((x >> (16 * k)) & 0xffffu), f = s + (k ? high : low);
                 if (!live || s == 0) continue;
-                if (value && (s >= 0x7f80 || f < 128 || f >= 28 * 128)) sm.bad[span & 3] = span;
+                if (value && (s >= 0x7f80 || f < 128 || f >= 28 * 128)) odd |= kValues;
                 else if (s >= 0x7f80) d |= 0x7e00u << (16 * k);
                 else if (s >= 128 && f >= 128) d |= (uint32_t)(f << 3) << (16 * k);
               }
@@ -377,7 +398,15 @@ attend_tc(const __grid_constant__ AttendArgs a, const __grid_constant__ CacheVie
                 (i ? vs[1][e][w] : vs[0][e][w]) = d;
               }
           }
+          odd = __reduce_or_sync(kAll, odd);
+          if (odd & kValues) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+              for (int w = 0; w < Dv / 64; ++w) vs[i][0][w] = vs[i][1][w] = 0;
+          }
         }
+        if (lane == 0) sm.odd[st][pw] = (uint8_t)odd;
         // ---- codes: keys to row 8 i + g, chunk (w % 2) 4 + q; values to rows 8 i + 2 q + e, chunk g
         char *k_to = reinterpret_cast<char *>(sm.k[st][0]) + (pw * 16 + g) * 128;
         char *v_to = reinterpret_cast<char *>(sm.v[st][0]) + (pw * 16 + 2 * q) * 128;
@@ -443,12 +472,15 @@ attend_tc(const __grid_constant__ AttendArgs a, const __grid_constant__ CacheVie
       auto values = [&](uint32_t u) {  // O += P V' of tile u
         if (!wait(&sm.p_full[u & 1], u >> 1)) return;
         tc_fence_after();
+        // O begins with the first tile's products, or with what the softmax warps have put there
+        const uint2 odd = *reinterpret_cast<const uint2 *>(sm.odd[u & 1]);
+        const bool begun = u > it0 || ((odd.x | odd.y) & (0x01010101u * kValues));
         if (lane == 0) {
           constexpr uint32_t id = idesc_f16(kTcRows, Dv) | (1u << 16);
           for (int kk = 0; kk < kTok / 16; ++kk) {
             const uint32_t p = tmem + kS + (u & 1) * 128 + kk * 16;
             const uint64_t rows = sdesc_mn(sm.v[u & 1][0] + kk * 16 * 64);
-            tc_mma_ts(tmem + kO, p, rows, id, u > it0 || kk > 0 ? 1u : 0u);
+            tc_mma_ts(tmem + kO, p, rows, id, begun || kk > 0 ? 1u : 0u);
             tc_mma_ts(tmem + kO, p + 8, rows, id, 1u);
           }
           tc_commit(&sm.kv_empty[u & 1]);
@@ -531,10 +563,9 @@ attend_tc(const __grid_constant__ AttendArgs a, const __grid_constant__ CacheVie
         if (!wait(&sm.kv_full[st], it >> 1) || !wait(&sm.s_full[st], it >> 1)) break;
         tc_fence_after();
         const int left = see - t * kTok;
-        int gone = 0;
-#pragma unroll
-        for (int k = 0; k < kProducers; ++k) gone |= sm.gone[st][k] << k;
-        const bool edge = see_all - t * kTok < kTok || gone;
+        const uint2 odd = *reinterpret_cast<const uint2 *>(sm.odd[st]);
+        auto is = [&](int c, uint32_t what) { return ((c < 4 ? odd.x : odd.y) >> (8 * (c & 3))) & what; };
+        const bool edge = see_all - t * kTok < kTok || ((odd.x | odd.y) & (0x01010101u * kGone));
         // to logits in units of log 2
         auto to2 = [&](int c) { return fmaxf(sm.scale[st][c] * rf, 1e-37f); };
         float sums[2] = {0.f, 0.f};
@@ -608,20 +639,46 @@ attend_tc(const __grid_constant__ AttendArgs a, const __grid_constant__ CacheVie
           }
           tmem_st32(col + c * 16, w);
         };
-        if (__builtin_expect(edge, 0)) {
+        const bool values = (odd.x | odd.y) & (0x01010101u * kValues);
+        if (__builtin_expect(edge || values, 0)) {
+          // where V' does not hold all values, the reference for the whole tile first, and these
+          // tokens' values by their logits
+          float all = -CUDART_INF_F;
 #pragma unroll 1
-          for (int c = 0; c < 8; c += 2) {
+          for (int c = values ? -8 : 0; c < 8; c += 2) {
+            if (c == 0 && values) {
+              if (__any_sync(kAll, all > mx + 14.f)) move(all, 0);
+              if (it > it0 && ok) {
+                wait(&sm.kv_empty[(it - 1) & 1], (it - 1) >> 1);
+                tc_fence_after();
+              }
+              bool begin = it == it0;
+#pragma unroll 1
+              for (int k = 0; k < 8 && ok; ++k) {
+                if (!is(k, kValues)) continue;
+                const uint8_t *p = cache_tile(v, cur.b, cur.hk, 4 * t + (k >> 1), S::kBytes);
+                if (!p) continue;
+                exact_values<D, Dv>(col + k * 16, to2(k), mx == -CUDART_INF_F ? 0.f : mx, left - 16 * k, p,
+                                    k & 1, sm.unit[span & 3], tmem + lane_base + kO, sm.tokens[warp], begin);
+                begin = false;
+              }
+              if (!ok) break;
+            }
             uint32_t x[2][16];
-            tmem_ld16_async(col + c * 16, x[0]);
-            tmem_ld16_async(col + c * 16 + 16, x[1]);
+            tmem_ld16_async(col + (c & 7) * 16, x[0]);
+            tmem_ld16_async(col + (c & 7) * 16 + 16, x[1]);
             arrived(x[0]);
             arrived(x[1]);
 #pragma unroll
-            for (int k = 0; k < 2; ++k)
+            for (int k = 0; k < 2; ++k) {
+              const int n = is((c & 7) + k, kGone) ? 0 : left - 16 * ((c & 7) + k);
 #pragma unroll
               for (int e = 0; e < 16; ++e)
-                if (16 * (c + k) + e >= left || (gone >> (c + k)) & 1) x[k][e] = 0xff800000u;  // -infinity
-            const float top = top_of(c, x);
+                if (e >= n) x[k][e] = 0xff800000u;  // -infinity
+            }
+            const float top = top_of(c & 7, x);
+            all = fmaxf(all, top);
+            if (c < 0) continue;
             if (__any_sync(kAll, top > mx + 14.f)) move(top, c);
             weigh(c, x);
           }
@@ -657,68 +714,34 @@ attend_tc(const __grid_constant__ AttendArgs a, const __grid_constant__ CacheVie
       const int slot = 2 * blockIdx.x + (span > 1 ? 1 : 0);
       if (cur.t0 == 0 && tid == 0)
         a.ends[((int64_t)cur.b * v.Hkv + cur.hk) * a.nrb + cur.rb] = make_int2(slot, blockIdx.x + cur.parts_in - 1);
-      if (*reinterpret_cast<volatile int *>(&sm.bad[span & 3]) != span) {
 #pragma unroll 1
-        for (int c0 = 0; c0 < Dv; c0 += 64) {
-          float y[64];
-          __syncwarp();  // lanes without a row have not stored: the loads below take the whole warp
+      for (int c0 = 0; c0 < Dv; c0 += 64) {
+        float y[64];
+        __syncwarp();  // lanes without a row have not stored: the loads below take the whole warp
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            float o[16];
-            tmem_ld16(tmem + lane_base + kO + c0 + c * 16, o);
+        for (int c = 0; c < 4; ++c) {
+          float o[16];
+          tmem_ld16(tmem + lane_base + kO + c0 + c * 16, o);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) y[c * 16 + e] = o[e];
-          }
-          if (!live) continue;
-#pragma unroll
-          for (int c = 0; c < 64; c += 4) {
-            const float back = 1.f / sm.unit[span & 3][(c0 + c) / 32];
-            float z[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) z[e] = y[column_of(c + e)] * back;
-            if (whole) {
-              finish_row<__nv_bfloat16>(a, cur.b, h, m, c0 + c, z, l, mx);
-            } else {
-              const int64_t at = (int64_t)slot * kTcRows + tid;
-              *reinterpret_cast<float4 *>(a.part + at * Dv + c0 + c) = make_float4(z[0], z[1], z[2], z[3]);
-              if (c0 + c == 0) *reinterpret_cast<float2 *>(a.part_ml + at * 2) = make_float2(mx, l);
-            }
-          }
+          for (int e = 0; e < 16; ++e) y[c * 16 + e] = o[e];
         }
-        tc_fence_before();
-      } else {
-        // a step outside what V' holds: the rows again, one warp a row
-        for (int r = warp; r < kTcRows; r += kSoftmaxWarps) {
-          const int gr2 = cur.rb * kTcRows + r;
-          const int m2 = gr2 / a.G, h2 = cur.hk * a.G + (gr2 - m2 * a.G);
-          if (m2 >= cur.rows) continue;
-          const __nv_bfloat16 *src =
-              (const __nv_bfloat16 *)a.Q.p + cur.b * a.Q.sb + h2 * a.Q.sh + m2 * a.Q.sn;
-          float *qs = sm.slow_q[warp];
-          __syncwarp();
-          for (int c = lane; c < D; c += 32) qs[c] = __bfloat162float(src[c]) * a.scale * 1.44269504f;
-          __syncwarp();
-          float mr, lr, o[NG];
-          slow_row<D, Dv>(a, v, cur.b, cur.hk, min(max(cur.len - cur.rows + m2 + 1, 0), cur.len), 4 * cur.t0,
-                          4 * cur.t1, qs, mr, lr, o);
-          const float at0 = mr == -CUDART_INF_F ? 0.f : mr;
+        if (!live) continue;
 #pragma unroll
-          for (int k = 0; k < NG; ++k) {
-            const int c = 32 * k + lane;
-            if (whole) {
-              ((__nv_bfloat16 *)a.O.p + cur.b * a.O.sb + h2 * a.O.sh + m2 * a.O.sn)[c] =
-                  __float2bfloat16_rn(lr == 0.f ? 0.f : o[k] / lr);
-              if (c == 0 && a.lse)
-                a.lse[((int64_t)cur.b * a.H + h2) * a.M + m2] =
-                    lr == 0.f ? -CUDART_INF_F : (at0 + log2f(lr)) * 0.693147181f;
-            } else {
-              const int64_t at = (int64_t)slot * kTcRows + r;
-              a.part[at * Dv + c] = o[k];
-              if (c == 0) *reinterpret_cast<float2 *>(a.part_ml + at * 2) = make_float2(mr, lr);
-            }
+        for (int c = 0; c < 64; c += 4) {
+          const float back = 1.f / sm.unit[span & 3][(c0 + c) / 32];
+          float z[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) z[e] = y[column_of(c + e)] * back;
+          if (whole) {
+            finish_row<__nv_bfloat16>(a, cur.b, h, m, c0 + c, z, l, mx);
+          } else {
+            const int64_t at = (int64_t)slot * kTcRows + tid;
+            *reinterpret_cast<float4 *>(a.part + at * Dv + c0 + c) = make_float4(z[0], z[1], z[2], z[3]);
+            if (c0 + c == 0) *reinterpret_cast<float2 *>(a.part_ml + at * 2) = make_float2(mx, l);
           }
         }
       }
+      tc_fence_before();
     }
   }
   // products still in flight land before shared memory and TMEM go: the last commit tracks them all

@@ -855,3 +855,64 @@ def test_values_that_begin_with_zeros(H, M, D, Dv):
     # (recomputing a stretch on the CUDA cores took a hundred times as long)
     assert duration(call) < 5 * plain + 0.05
     ok()
+
+
+@pytest.mark.parametrize("D,Dv", WIDTHS)
+@pytest.mark.parametrize("H,M", [(4, 4), (4, 40), (2, 128)])
+@pytest.mark.parametrize("odd", [[3], [0, 127, 128, 300], [200, 201, 260, 599], list(range(250, 290)) + [598]])
+def test_a_few_values_of_another_size_count_by_their_weight(odd, H, M, D, Dv):
+    """Tokens whose values are 2^40 times the others' and whose logits are so far below that both count,
+    a few whose values are 2^-40 times, and a NaN: in the first tile of a stretch, at its end, behind
+    what the earlier rows see.  Weights of 2^-40 of the largest count in full (float32 arithmetic: the
+    bound of fine_close, its absolute term by the ordinary values)."""
+    T = 600
+    s = Store(1, 1, 32, 20, D, Dv)
+    K, V = randn(1, 1, 1, T, D) * 0.2, randn(2, 1, 1, T, Dv)
+    K[0, 0, odd] = -1.0
+    V[0, 0, odd] *= 2.0 ** 40
+    V[0, 0, 77:80] *= 2.0 ** -40
+    m.muse_cache_write(s.cache, K, V, s.table, ints([0]))
+    Q = (torch.ones(1, H, M, D, device="cuda") + 0.1 * randn(3, 1, H, M, D)).to(BF16)
+    scale = 28.0 / D                       # logits of the odd ones about -28: 2^-40
+    out, _ = m.muse_cache_attend(Q, s.cache, s.table, ints([T]), scale=scale)
+    Kh, Vh = s.values()
+    ref, _, A, X = so.cache_attend(host(Q), Kh, Vh, [T], [M], scale)
+    usual = np.delete(Vh[0][:, :T], odd, 1)
+    e = (42 * U * X + 4 * U)[..., None]
+    tol = HALF[BF16] * np.abs(ref) + A * (2 * e + 2.0 ** -20 + 2 * U * (T / 16 + 40)) \
+        + np.abs(usual).max() * T * 2.0 ** -29
+    d = np.abs(host(out) - ref)
+    assert (d <= tol).all(), (int((d > tol).sum()), float((d / tol).max()))
+    V[0, 0, T - 2, 40] = float("nan")
+    m.muse_cache_write(s.cache, K, V, s.table, ints([0]))
+    bad = torch.isnan(m.muse_cache_attend(Q, s.cache, s.table, ints([T]), scale=scale)[0])
+    sees = torch.arange(T - M, T).cuda() >= T - 2
+    want = sees[:, None] & (torch.arange(Dv).cuda() // 32 == 1)
+    assert torch.equal(bad, want.expand(1, H, M, Dv))
+    ok()
+
+
+@pytest.mark.parametrize("what", ["nan", "large", "growing"])
+@pytest.mark.parametrize("M", [4, 40])
+def test_values_of_another_size_cost_little(M, what):
+    """One NaN or one large value of a long sequence takes about the time of ordinary values, and
+    values that grow along the sequence a few times that (the stretch, or the rest of it, was
+    recomputed: a hundred times)."""
+    B, Hkv, T = 2, 2, 8192
+    s = Store(B, Hkv, 64, 128, 128, 128)
+    K, V = randn(1, B, Hkv, T, 128), randn(2, B, Hkv, T, 128)
+    Q = randn(3, B, 8, M, 128, dtype=BF16)
+    call = lambda: m.muse_cache_attend(Q, s.cache, s.table, ints([T, T]), scale=0.1)
+    m.muse_cache_write(s.cache, K, V, s.table, ints([0] * B))
+    plain = duration(call)
+    if what == "growing":
+        V *= 2.0 ** torch.linspace(-30, 30, T, device="cuda")[:, None]
+    else:
+        V[:, :, 5000, 7] = float("nan") if what == "nan" else 1e9
+    m.muse_cache_write(s.cache, K, V, s.table, ints([0] * B))
+    assert duration(call) < (16 if what == "growing" else 3) * plain + 0.05
+    if what == "large":                  # where many stretches begin
+        V[:, :, ::512, 7] = 1e9
+        m.muse_cache_write(s.cache, K, V, s.table, ints([0] * B))
+        assert duration(call) < 4 * plain + 0.05
+    ok()
