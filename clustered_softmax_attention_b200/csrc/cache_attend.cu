@@ -490,7 +490,7 @@ attend(const __grid_constant__ AttendArgs a, const __grid_constant__ CacheView v
     // groups' steps, as bits, to that unit
     uint32_t shift[NG / 2];
     float unit[NG];
-    bool have_unit = false;
+    bool have_unit = false, far = false;
 
     int tok = (sp.t0 + ts) * kTile - TS * kTile;
     for (int it = 0; it < n_it; ++it) {
@@ -569,9 +569,10 @@ attend(const __grid_constant__ AttendArgs a, const __grid_constant__ CacheView v
         for (int e = 0; e < 2; ++e) {
           const float(&p)[4][2] = tk.p[nb];
           top[nb][e] = fmaxf(fmaxf(p[0][e], p[1][e]), fmaxf(p[2][e], p[3][e]));
-          move |= top[nb][e] * rf[nb][e] > mx[nb][e] + 14.f;
+          move |= __fmul_rn(top[nb][e], rf[nb][e]) - mx[nb][e] > 14.f;
         }
       if (__builtin_expect(__any_sync(kAll, move), 0)) {
+        far = false;
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -580,9 +581,10 @@ attend(const __grid_constant__ AttendArgs a, const __grid_constant__ CacheView v
             y = fmaxf(y, __shfl_xor_sync(kAll, y, 4));
             y = fmaxf(y, __shfl_xor_sync(kAll, y, 8));
             y = fmaxf(y, __shfl_xor_sync(kAll, y, 16));
-            const float now = fmaxf(mx[nb][e], y * rf[nb][e] - 9.f);
+            const float now = fmaxf(mx[nb][e], __fsub_ru(__fmul_rn(y, rf[nb][e]), 9.f));
             const float fix = now == -CUDART_INF_F ? 1.f : ex2(mx[nb][e] - now);
             mx[nb][e] = now;
+            far |= fabsf(now) > kFar && now != -CUDART_INF_F;
             l[nb][e] *= fix;
 #pragma unroll
             for (int j = 0; j < Dv / 16; ++j) {
@@ -590,14 +592,25 @@ attend(const __grid_constant__ AttendArgs a, const __grid_constant__ CacheView v
               acc.o[nb][j][2 + e] *= fix;
             }
           }
+        far = __any_sync(kAll, far);
       }
+      if (__builtin_expect(far, 0)) {
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
+        for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+          for (int i = 0; i < 4; ++i)
 #pragma unroll
-          for (int e = 0; e < 2; ++e)
-            tk.p[nb][i][e] = ex2(fmaf(tk.p[nb][i][e], rf[nb][e], -mx[nb][e]));
+            for (int e = 0; e < 2; ++e)
+              tk.p[nb][i][e] = ex2(__fmul_rn(tk.p[nb][i][e], rf[nb][e]) - mx[nb][e]);
+      } else {
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              tk.p[nb][i][e] = ex2(fmaf(tk.p[nb][i][e], rf[nb][e], -mx[nb][e]));
+      }
       if (__builtin_expect(hide.edge, 0)) {
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)

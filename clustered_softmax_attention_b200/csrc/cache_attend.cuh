@@ -171,6 +171,10 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// A weight is 2^(x r - m), in one rounding; beyond 2^20 that is no longer by the rounded logits x r that
+// the reference m was taken from (half a step of 2^28 is 16), so there x r is rounded first.  m itself,
+// 9 below a logit, is rounded upwards, so that no weight passes 2^14.
+constexpr float kFar = 0x1p20f;
 // (x & mask) | with in one operation (written out, it becomes two).
 template <uint32_t kMask>
 __device__ __forceinline__ uint32_t picked(uint32_t x, uint32_t with) {

@@ -147,7 +147,7 @@ __device__ __noinline__ void exact_values(uint32_t logits, float to2, float ref,
     }
 #pragma unroll 1
     for (int t = 0; t < 16; ++t) {
-      const float w = ex2(fmaf(tmem_ld1(logits + t), to2, -ref));
+      const float w = ex2(__fmul_rn(tmem_ld1(logits + t), to2) - ref);
       if (t < left) {  // whatever others hold
 #pragma unroll
         for (int e = 0; e < 16; e += 4) {
@@ -557,6 +557,7 @@ attend_tc(const __grid_constant__ AttendArgs a, const __grid_constant__ CacheVie
       mbar_arrive(&sm.q_full);
 
       float mx = -CUDART_INF_F, l = 0.f;
+      bool far = false;  // of any row of the warp
       const uint32_t it0 = it;
       for (int t = cur.t0; t < cur.t1 && ok; ++t, ++it) {
         const uint32_t st = it & 1, col = tmem + lane_base + kS + st * 128;
@@ -572,9 +573,10 @@ attend_tc(const __grid_constant__ AttendArgs a, const __grid_constant__ CacheVie
         // The reference moves: what was summed and weighed by it, the tile's first `done` chunks of
         // weights among them, is brought to the new one.
         auto move = [&](float top, int done) {
-          const float now = fmaxf(mx, top - 9.f);
+          const float now = fmaxf(mx, __fsub_ru(top, 9.f));
           const float fix = now == -CUDART_INF_F ? 1.f : ex2(mx - now);
           mx = now;
+          far = __any_sync(kAll, fabsf(now) > kFar && now != -CUDART_INF_F);
           l *= fix;
           sums[0] *= fix;
           sums[1] *= fix;
@@ -623,12 +625,12 @@ attend_tc(const __grid_constant__ AttendArgs a, const __grid_constant__ CacheVie
           }
           return top;
         };
-        auto weigh = [&](int c, const uint32_t (&x)[2][16]) {
+        auto weigh = [&](int c, const uint32_t (&x)[2][16], bool scaled) {
           const float ref = mx == -CUDART_INF_F ? 0.f : mx;
           uint32_t w[32];  // the two chunks' upper and lower pieces
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            const float f = to2(c + k);
+            const float f = scaled ? 1.f : to2(c + k);
 #pragma unroll
             for (int e = 0; e < 16; e += 2) {
               const float p0 = ex2(fmaf(__uint_as_float(x[k][e]), f, -ref));
@@ -640,49 +642,10 @@ attend_tc(const __grid_constant__ AttendArgs a, const __grid_constant__ CacheVie
           tmem_st32(col + c * 16, w);
         };
         const bool values = (odd.x | odd.y) & (0x01010101u * kValues);
-        if (__builtin_expect(edge || values, 0)) {
-          // where V' does not hold all values, the reference for the whole tile first, and these
-          // tokens' values by their logits
-          float all = -CUDART_INF_F;
-#pragma unroll 1
-          for (int c = values ? -8 : 0; c < 8; c += 2) {
-            if (c == 0 && values) {
-              if (__any_sync(kAll, all > mx + 14.f)) move(all, 0);
-              if (it > it0 && ok) {
-                wait(&sm.kv_empty[(it - 1) & 1], (it - 1) >> 1);
-                tc_fence_after();
-              }
-              bool begin = it == it0;
-#pragma unroll 1
-              for (int k = 0; k < 8 && ok; ++k) {
-                if (!is(k, kValues)) continue;
-                const uint8_t *p = cache_tile(v, cur.b, cur.hk, 4 * t + (k >> 1), S::kBytes);
-                if (!p) continue;
-                exact_values<D, Dv>(col + k * 16, to2(k), mx == -CUDART_INF_F ? 0.f : mx, left - 16 * k, p,
-                                    k & 1, sm.unit[span & 3], tmem + lane_base + kO, sm.tokens[warp], begin);
-                begin = false;
-              }
-              if (!ok) break;
-            }
-            uint32_t x[2][16];
-            tmem_ld16_async(col + (c & 7) * 16, x[0]);
-            tmem_ld16_async(col + (c & 7) * 16 + 16, x[1]);
-            arrived(x[0]);
-            arrived(x[1]);
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const int n = is((c & 7) + k, kGone) ? 0 : left - 16 * ((c & 7) + k);
-#pragma unroll
-              for (int e = 0; e < 16; ++e)
-                if (e >= n) x[k][e] = 0xff800000u;  // -infinity
-            }
-            const float top = top_of(c & 7, x);
-            all = fmaxf(all, top);
-            if (c < 0) continue;
-            if (__any_sync(kAll, top > mx + 14.f)) move(top, c);
-            weigh(c, x);
-          }
-        } else {
+        // Most tiles: nothing hidden, nothing odd, and the reference stays.  Chunks from `begun` on are left
+        // to the loop below, which does everything and is kept small.
+        int begun = values ? -8 : 0;
+        if (__builtin_expect(!(edge || values || far), 1)) {
           uint32_t x[2][2][16];
           tmem_ld16_async(col, x[0][0]);
           tmem_ld16_async(col + 16, x[0][1]);
@@ -691,14 +654,62 @@ attend_tc(const __grid_constant__ AttendArgs a, const __grid_constant__ CacheVie
             const int k = (c >> 1) & 1;
             arrived(x[k][0]);
             arrived(x[k][1]);
-            const float top = top_of(c, x[k]);
-            if (__builtin_expect(__any_sync(kAll, top > mx + 14.f), 0)) move(top, c);
+            if (__any_sync(kAll, top_of(c, x[k]) - mx > 14.f)) break;
             if (c < 6) {
               tmem_ld16_async(col + (c + 2) * 16, x[k ^ 1][0]);
               tmem_ld16_async(col + (c + 3) * 16, x[k ^ 1][1]);
             }
-            weigh(c, x[k]);
+            weigh(c, x[k], false);
+            begun = c + 2;
           }
+        }
+        // where V' does not hold all values: the reference for the whole tile first (c below 0), and
+        // these tokens' values by their logits
+        float all = -CUDART_INF_F;
+#pragma unroll 1
+        for (int c = begun; c < 8; c += 2) {
+          if (c == 0 && values) {
+            if (__any_sync(kAll, all - mx > 14.f)) move(all, 0);
+            if (it > it0 && ok) {
+              wait(&sm.kv_empty[(it - 1) & 1], (it - 1) >> 1);
+              tc_fence_after();
+            }
+            bool begin = it == it0;
+#pragma unroll 1
+            for (int k = 0; k < 8 && ok; ++k) {
+              if (!is(k, kValues)) continue;
+              const uint8_t *p = cache_tile(v, cur.b, cur.hk, 4 * t + (k >> 1), S::kBytes);
+              if (!p) continue;
+              exact_values<D, Dv>(col + k * 16, to2(k), mx == -CUDART_INF_F ? 0.f : mx, left - 16 * k, p,
+                                  k & 1, sm.unit[span & 3], tmem + lane_base + kO, sm.tokens[warp], begin);
+              begin = false;
+            }
+          }
+          if (!ok) break;
+          uint32_t x[2][16];
+          tmem_ld16_async(col + (c & 7) * 16, x[0]);
+          tmem_ld16_async(col + (c & 7) * 16 + 16, x[1]);
+          arrived(x[0]);
+          arrived(x[1]);
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const int n = is((c & 7) + k, kGone) ? 0 : left - 16 * ((c & 7) + k);
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              if (e >= n) x[k][e] = 0xff800000u;  // -infinity
+          }
+          const float top = top_of(c & 7, x);
+          all = fmaxf(all, top);
+          if (c < 0) continue;
+          if (__any_sync(kAll, top - mx > 14.f)) move(top, c);
+          if (far) {
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+              for (int e = 0; e < 16; ++e)
+                x[k][e] = __float_as_uint(__fmul_rn(__uint_as_float(x[k][e]), to2(c + k)));
+          }
+          weigh(c, x, far);
         }
         if (!ok) break;
         tmem_st_wait();

@@ -916,3 +916,29 @@ def test_values_of_another_size_cost_little(M, what):
         m.muse_cache_write(s.cache, K, V, s.table, ints([0] * B))
         assert duration(call) < 4 * plain + 0.05
     ok()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("size", [2.0 ** 18, 2.0 ** 21, 2.0 ** 24, 2.0 ** 26, 2.0 ** 30])
+@pytest.mark.parametrize("H,M", [(4, 1), (4, 16), (4, 40)])
+def test_logits_far_from_zero(H, M, size, dtype):
+    """Logits of either sign, of which float32 holds no fractions: the largest rounded ones share the
+    row (attend_close: where X u is a step or more, any weights whose sum is one are right; what is not
+    is a NaN, or a sum above the largest value)."""
+    T = 300
+    s = Store(2, 1, 32, 10, 64, 64)
+    K, V = randn(1, 2, 1, T, 64), randn(2, 2, 1, T, 64)
+    K[0] *= size
+    K[1] = -size * (3 + 2.0 ** -8 * torch.arange(T, device="cuda")[:, None])
+    m.muse_cache_write(s.cache, K, V, s.table, ints([0, 0]))
+    Q = randn(3, 2, H, M, 64).abs().to(dtype)
+    K, V = s.values()
+    for length in (T, 129):
+        out, lse = m.muse_cache_attend(Q, s.cache, s.table, ints([length] * 2), scale=0.25)
+        ref, rl, A, X = so.cache_attend(host(Q), K, V, [length] * 2, [M] * 2, 0.25)
+        assert torch.isfinite(out).all() and torch.isfinite(lse).all()
+        # (42 u) X as in attend_close; log sums below log T
+        assert (np.abs(host(lse) - rl) <= 42 * U * X + 4 * U * np.abs(rl) + 6).all()
+        top = np.abs(V[:, :, :length]).max((1, 2))[:, None, None, :]
+        assert (np.abs(host(out)) <= top * (1 + 2.0 ** -7)).all()
+    ok()
