@@ -10,7 +10,8 @@
 // S of the next tile is issued before O += P V' of this one, so the softmax of one tile runs
 // beside both products.
 //   K' = code step 2^(12 - e), e the exponent of the largest step of sixteen tokens: exact for
-//   steps down to 2^-26 of that, off by 2^-37 of it below; 2^(e - 12) multiplies their columns of S.
+//   steps down to 2^-26 of that; 2^(e - 12) multiplies their columns of S.  With a smaller step (zero
+//   apart) the softmax warps form the sixteen tokens' logits in float32 from the codes.
 //   V' = code step unit[group], a power of two that the group's first tile of the span that is not all
 //   zeros sets by its usual largest step: exact for steps from 2^-17 to 2^9 of that.  Sixteen tokens with
 //   a step outside of it (zero apart) have V' = 0, and the softmax warps add p v to O in float32 from
@@ -42,6 +43,7 @@ constexpr int kThreads = 32 * (kIssuer + 1);
 constexpr uint32_t kTmemCols = 512;
 constexpr int kGone = 1;    // not in the cache
 constexpr int kValues = 2;  // value steps that V' does not hold: it holds zeros
+constexpr int kKeys = 4;    // key steps that K' does not hold
 // TMEM columns: S (two of 128), O.  A weight takes the place of its S as two float16 pieces, 21 bits:
 // sixteen tokens' columns hold eight of upper and eight of lower pieces.  In one piece (11 bits) results
 // differed from float32 arithmetic's by 9e-4 in norm, in two by 1.6e-4.  One piece and two, 128 + 128
@@ -60,8 +62,8 @@ struct __align__(1024) Smem {
   float unit[4][Dv / 32];     // by span
   alignas(4) uint16_t big[2][kProducers][Dv / 32];  // by exchange
   int exps[kTcRows];          // of the queries' powers of two
-  float tokens[kSoftmaxWarps][16 * 16];  // sixteen tokens' values, sixteen columns of O at a time
-  alignas(8) uint8_t odd[2][kProducers];  // kGone, kValues: what holds of sixteen tokens
+  float tokens[kSoftmaxWarps][16 * 16];  // sixteen tokens' keys or values, sixteen channels at a time
+  alignas(8) uint8_t odd[2][kProducers];  // kGone, kValues, kKeys: what holds of sixteen tokens
   int64_t run[kThreads + kThreads / 32];
   uint64_t q_full, unit_full, kv_full[2], kv_empty[2], s_full[2], p_full[2], end;
   uint32_t tmem_base;
@@ -111,6 +113,54 @@ __device__ __forceinline__ uint4 *chunk(__half *block, int row, int c) {
 // Column of O (within 64) that holds channel c of 64.
 __host__ __device__ constexpr int column_of(int c) {
   return 8 * (c % 8) + (c / 8 < 4 ? 2 * (c / 8) : 2 * (c / 8 - 4) + 1);
+}
+
+// The columns of S of sixteen tokens whose key steps K' does not hold, in float32 from the codes: a row a
+// thread, `q` its block of queries.  `p`: their tile of 32 tokens, whose half `part` they are; `scale`: what
+// the columns are multiplied by.  Small rather than fast (5 us), as exact_values.
+template <int D>
+__device__ __noinline__ void exact_logits(uint32_t columns, __half (*q)[kTcRows * 64], const uint8_t *p,
+                                          const uint16_t *steps, int part, float scale, float *tokens) {
+  const int lane = threadIdx.x & 31, t0 = 16 * part + (lane >> 1), e = -ilogbf(scale);
+  const uint32_t *kw = reinterpret_cast<const uint32_t *>(p);
+#pragma unroll 1
+  for (int j = 0; j < D / 16; ++j) {
+    // a lane a token and one of its words, the channels in the queries' order
+    const uint32_t word = kw[key_word<D>(t0, 2 * (j & 1) + (lane & 1), j >> 1)];
+    const float f = ldexpf(step_value(steps[t0 * (D / 32) + (j >> 1)]), e);
+    float y[8];
+#pragma unroll
+    for (int n = 0; n < 8; ++n) y[2 * (n & 3) + (n >> 2)] = code_value(word, n) * f;
+    __syncwarp();  // the last channels have been read
+    float4 *to = reinterpret_cast<float4 *>(tokens + (lane >> 1) * 16 + (lane & 1) * 8);
+    to[0] = make_float4(y[0], y[1], y[2], y[3]);
+    to[1] = make_float4(y[4], y[5], y[6], y[7]);
+    __syncwarp();
+    float x[16];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint4 u = *chunk(q[j >> 2], threadIdx.x, (2 * j + h) & 7);
+      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 z = __half22float2(halves(w[k]));
+        x[8 * h + 2 * k] = z.x;
+        x[8 * h + 2 * k + 1] = z.y;
+      }
+    }
+#pragma unroll 1
+    for (int t = 0; t < 16; ++t) {
+      float s = 0.f;
+#pragma unroll
+      for (int c = 0; c < 16; c += 4) {
+        const float4 k = *reinterpret_cast<const float4 *>(tokens + t * 16 + c);
+        s = fmaf(x[c], k.x, fmaf(x[c + 1], k.y, fmaf(x[c + 2], k.z, fmaf(x[c + 3], k.w, s))));
+      }
+      if (j) s += tmem_ld1(columns + t);
+      tmem_st1(columns + t, s);
+    }
+    tmem_st_wait();
+  }
 }
 
 // O += p v of sixteen tokens whose value steps V' does not hold, in float32 from the codes: a row a
@@ -350,17 +400,16 @@ attend_tc(const __grid_constant__ AttendArgs a, const __grid_constant__ CacheVie
             vs[i][0][0] = y.x;
             vs[i][1][0] = y.y;
           }
-          // fields 12..27 of keys, 8..23 of values (18: the first tile's usual largest); n < 16 also goes
-          // the careful way, for the tokens that are not there.  k_shift is above zero where the largest
-          // is tiny, and a NaN (0xffff) comes back into range with it: its sign tells.
+          // fields 12..27 of keys, 8..23 of values (18: the first tile's usual largest).  Also the careful
+          // way go n < 16, for the tokens that are not there, and keys so small (e_top < 16) that the shift
+          // would bring steps without an exponent, or a NaN (0xffff), into range.
 #pragma unroll
-          for (int w = 0; w < NGk / 2; ++w)
-            off_range |= (ks[i][w] + k_shift - 0x06000600u) | (ks[i][w] & 0x80008000u);
+          for (int w = 0; w < NGk / 2; ++w) off_range |= ks[i][w] + k_shift - 0x06000600u;
 #pragma unroll
           for (int w = 0; w < Dv / 64; ++w)
             off_range |= (vs[i][0][w] + shift[w] - 0x04000400u) | (vs[i][1][w] + shift[w] - 0x04000400u);
         }
-        if (__builtin_expect(!__any_sync(kAll, (off_range & 0xf800f800u) != 0) && n >= 16, 1)) {
+        if (__builtin_expect(!__any_sync(kAll, (off_range & 0xf800f800u) != 0) && n >= 16 && e_top >= 16, 1)) {
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
 #pragma unroll
@@ -372,8 +421,8 @@ attend_tc(const __grid_constant__ AttendArgs a, const __grid_constant__ CacheVie
             }
           }
         } else {
-          // half by half: tokens that are not there and zero steps are zero; a key step too small is
-          // zero too, a NaN NaN; with a value step that float16 does not hold all values are zero here
+          // half by half: tokens that are not there and zero steps are zero, a key's NaN is NaN; with a value
+          // step that float16 does not hold all values are zero here
 #pragma unroll 1
           for (int i = 0; i < 2; ++i) {
             auto careful = [&](uint32_t x, uint32_t by, bool live, bool value) {
@@ -382,9 +431,10 @@ attend_tc(const __grid_constant__ AttendArgs a, const __grid_constant__ CacheVie
               for (int k = 0; k < 2; ++k) {
                 const int s = (int)((x >> (16 * k)) & 0xffffu), f = s + (k ? high : low);
                 if (!live || s == 0) continue;
-                if (value && (s >= 0x7f80 || f < 128 || f >= 28 * 128)) odd |= kValues;
+                if (value && (s >= 0x7f80 || s < 128 || f < 128 || f >= 28 * 128)) odd |= kValues;
                 else if (s >= 0x7f80) d |= 0x7e00u << (16 * k);
-                else if (s >= 128 && f >= 128) d |= (uint32_t)(f << 3) << (16 * k);
+                else if (s < 128 || f < 128) odd |= kKeys;  // (of values: above)
+                else d |= (uint32_t)(f << 3) << (16 * k);
               }
               return d;
             };
@@ -641,6 +691,15 @@ attend_tc(const __grid_constant__ AttendArgs a, const __grid_constant__ CacheVie
           }
           tmem_st32(col + c * 16, w);
         };
+        if (__builtin_expect((odd.x | odd.y) & (0x01010101u * kKeys), 0)) {
+#pragma unroll 1
+          for (int k = 0; k < 8; ++k) {
+            const uint8_t *p = is(k, kKeys) ? cache_tile(v, cur.b, cur.hk, 4 * t + (k >> 1), S::kBytes) : nullptr;
+            if (p)
+              exact_logits<D>(col + k * 16, sm.q, p, reinterpret_cast<const uint16_t *>(p + S::kKStep), k & 1,
+                              sm.scale[st][k], sm.tokens[warp]);
+          }
+        }
         const bool values = (odd.x | odd.y) & (0x01010101u * kValues);
         // Most tiles: nothing hidden, nothing odd, and the reference stays.  Chunks from `begun` on are left
         // to the loop below, which does everything and is kept small.

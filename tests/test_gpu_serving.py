@@ -942,3 +942,35 @@ def test_logits_far_from_zero(H, M, size, dtype):
         top = np.abs(V[:, :, :length]).max((1, 2))[:, None, None, :]
         assert (np.abs(host(out)) <= top * (1 + 2.0 ** -7)).all()
     ok()
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("H,M", [(4, 4), (4, 40), (2, 128)])
+@pytest.mark.parametrize("what", ["newest", "group", "tiny", "next to nothing"])
+def test_keys_of_very_different_sizes_keep_their_logits(what, H, M, D):
+    """The newest tokens' keys 2^30 times their neighbours', which earlier rows do not see; a group of
+    channels 2^30 times the others where the queries are zero; a token's keys 2^-30 times the others',
+    and all keys below 2^-126, with queries as far above: every row by what it sees (attend_close)."""
+    T = 300
+    s = Store(1, 1, 32, 10, D, 64)
+    K, V = randn(1, 1, 1, T, D), randn(2, 1, 1, T, 64)
+    Q = randn(3, 1, H, M, D)
+    scale = 0.1
+    if what == "newest":
+        K[..., T - 2:, :] *= 2.0 ** 30
+    elif what == "group":
+        K[..., :32] *= 2.0 ** 30
+        Q[..., :32] = 0
+    elif what == "tiny":
+        K[..., 200:203, :] *= 2.0 ** -30
+        K[..., 100:117, 32:] *= 2.0 ** -60
+    else:
+        K *= 2.0 ** -127
+        Q *= 2.0 ** 100
+        scale = 2.0 ** 24
+    m.muse_cache_write(s.cache, K, V, s.table, ints([0]))
+    Q = Q.to(BF16)
+    for length in (T, T - 1, 256):
+        out, lse = m.muse_cache_attend(Q, s.cache, s.table, ints([length]), scale=scale)
+        attend_close(host(out), host(lse), Q, s, [length], [M], scale, BF16)
+    ok()
