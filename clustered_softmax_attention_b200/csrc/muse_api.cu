@@ -331,7 +331,7 @@ extern "C" muse_status muse_last_device_status(muse_stream_t st) {
 }
 
 extern "C" muse_status muse_set_test_hooks(unsigned hooks, uint64_t wait_limit_ns) {
-  if (hooks & ~(unsigned)MUSE_TEST_WITHHOLD_VALUES) return MUSE_ERR_INVALID_ARG;
+  if (hooks & ~(unsigned)(MUSE_TEST_WITHHOLD_VALUES | MUSE_TEST_WITHHOLD_CACHE)) return MUSE_ERR_INVALID_ARG;
   if (cudaDeviceSynchronize() != cudaSuccess) return MUSE_ERR_CUDA;
   int words[3];
   words[0] = (int)hooks;

@@ -200,6 +200,7 @@ def muse_last_device_status() -> int:
 
 
 MUSE_TEST_WITHHOLD_VALUES = 1
+MUSE_TEST_WITHHOLD_CACHE = 4
 
 
 def muse_set_test_hooks(hooks: int = 0, wait_limit_ns: int = 0) -> None:

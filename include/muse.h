@@ -460,13 +460,16 @@ muse_status muse_last_device_status(muse_stream_t st);
  *     hooks = MUSE_TEST_WITHHOLD_VALUES: the refinement kernel (the tensor-core path of
  *       muse_dipole_refine, muse_forward, muse_causal_blocks) never loads its value
  *       tiles, so the waits for them can only run out;
- *     wait_limit_ns > 0: the limit of the refinement kernel's waits (default 2 s when 0).
+ *     hooks = MUSE_TEST_WITHHOLD_CACHE: muse_cache_attend's form for more than 64 bfloat16
+ *       rows a cache head never hands on a part of its cache tiles;
+ *     wait_limit_ns > 0: the limit of these two kernels' waits (default 2 s when 0).
  *   The outputs of a call that timed out are undefined.  hooks = 0, wait_limit_ns = 0
  *   restores normal operation.  Applies to the current device, synchronises it first,
  *   and is process-wide: not for use while other work runs on the device.  Unknown hook
  *   bits return MUSE_ERR_INVALID_ARG.
  */
 #define MUSE_TEST_WITHHOLD_VALUES 1u
+#define MUSE_TEST_WITHHOLD_CACHE 4u
 muse_status muse_set_test_hooks(unsigned hooks, uint64_t wait_limit_ns);
 
 /*

@@ -974,3 +974,32 @@ def test_keys_of_very_different_sizes_keep_their_logits(what, H, M, D):
         out, lse = m.muse_cache_attend(Q, s.cache, s.table, ints([length]), scale=scale)
         attend_close(host(out), host(lse), Q, s, [length], [M], scale, BF16)
     ok()
+
+
+@pytest.mark.parametrize("wait_limit_ns", [3_000_000, 0])
+@pytest.mark.parametrize("T", [300, 4000])
+def test_a_wait_that_runs_out_is_reported_and_leaves_the_next_call_right(T, wait_limit_ns):
+    """The many-row form with a part of its tiles withheld: every role winds down, the join finds no
+    ends in the workspace that it can read by, and the next call is right.  (0: the default limit of 2 s,
+    which all CTAs wait out together.)"""
+    s = filled(2, 1, 32, 126, 64, 128, T)
+    Q = randn(1, 2, 4, 40, 64, dtype=BF16)
+    ws = torch.empty(m.muse_workspace_size("muse_cache_attend", m.dims(Q, randn(0, 2, 4, 40, 128, dtype=BF16)), 1),
+                     dtype=torch.uint8, device="cuda")
+    call = lambda: m.muse_cache_attend(Q, s.cache, s.table, ints([T, T // 2]), scale=0.1, ws=ws)
+    ref = [x.clone() for x in call()]
+    ok()
+    m.muse_set_test_hooks(m.MUSE_TEST_WITHHOLD_CACHE, wait_limit_ns)
+    try:
+        ws.fill_(0xff)
+        a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        a.record()
+        call()
+        b.record()
+        status = m.muse_last_device_status()
+    finally:
+        m.muse_set_test_hooks(0, 0)
+    limit = (wait_limit_ns or 2_000_000_000) * 1e-6
+    assert status == 6 and limit <= a.elapsed_time(b) < 2 * limit + 50
+    assert all(torch.equal(x, y) for x, y in zip(call(), ref))
+    ok()

@@ -210,3 +210,10 @@ def test_binding_does_not_cut_flags_short(flags):
     x = torch.zeros(2, 4, 8, 64, dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="flags"):
         m.muse_rope_axes(x, torch.zeros(1, 8, dtype=torch.int32), [32], flags=flags)
+
+
+def test_the_hook_of_the_many_row_form_is_a_bit_of_its_own(lib):
+    """Its value, and that bits beside it are refused before the device is touched."""
+    assert m.MUSE_TEST_WITHHOLD_CACHE == 4 and m.MUSE_TEST_WITHHOLD_VALUES == 1
+    for bits in (2, 6, 8, 4 | 8, 1 << 31):
+        assert lib.muse_set_test_hooks(bits, 0) == 1
