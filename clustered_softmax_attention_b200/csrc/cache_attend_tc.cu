@@ -29,6 +29,8 @@
 //   2 x 2 heads, 16384 tokens:   36 rows 37 and 39, 64 rows 39 and 39; 68 rows 46 and 37, 512 rows 110 and 70
 //   8 x 8 heads, 16384 tokens:   36 rows 195 and 166, 64 rows 199 and 168; 68 rows 390 and 170, 512 rows 1390 and 602
 //   2 x 2 heads, 1024 tokens:    36 rows 21 and 27, 64 rows 21 and 29; 68 rows 24 and 27, 512 rows 32 and 33
+#include <atomic>
+
 #include "cache_attend.cuh"
 #include "tc_ptx.cuh"
 
@@ -838,11 +840,19 @@ template <int D, int Dv>
 cudaError_t launch_attend_tc(AttendArgs a, const CacheView &v, int *status, cudaStream_t st) {
   const auto kernel = attend_tc<D, Dv>;
   const size_t smem = sizeof(Smem<D, Dv>) + 1024;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  int dev = 0, sms = 0;
-  if (e == cudaSuccess) e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  // SMs of a device, looked up with the kernel's attribute once a device
+  static std::atomic<int> known[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  int sms = known[dev].load(std::memory_order_acquire);
+  if (!sms) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    known[dev].store(sms, std::memory_order_release);
+  }
   const int rows = a.G * a.M;
   a.nrb = (rows + kTcRows - 1) / kTcRows;
   a.block_log2 = 7;
