@@ -488,9 +488,14 @@ attend(const __grid_constant__ AttendArgs a, const __grid_constant__ CacheView v
     }
     // the accumulators of value group w hold O * unit[w], a power of two; shift: what takes two
     // groups' steps, as bits, to that unit
-    uint32_t shift[NG / 2];
+    uint32_t shift[NG / 2], open = (1u << NG) - 1;  // open: groups that have no unit yet
     float unit[NG];
-    bool have_unit = false, far = false;
+#pragma unroll
+    for (int w = 0; w < NG; ++w) {
+      unit[w] = 1.f;
+      shift[w >> 1] = 0;
+    }
+    bool far = false;
 
     int tok = (sp.t0 + ts) * kTile - TS * kTile;
     for (int it = 0; it < n_it; ++it) {
@@ -626,13 +631,13 @@ attend(const __grid_constant__ AttendArgs a, const __grid_constant__ CacheView v
         for (int e = 0; e < 2; ++e)
           l[nb][e] += (tk.p[nb][0][e] + tk.p[nb][1][e]) + (tk.p[nb][2][e] + tk.p[nb][3][e]);
 
-      // ---- value steps in the unit of the accumulators, which the first tile sets: its largest
-      // step comes to [2^-3, 2^-2)
+      // ---- value steps in the unit of the accumulators, which a group's first tile that is not all
+      // zeros sets (before it the sums are zero, and any unit is right): its largest step comes to
+      // [2^-3, 2^-2)
       uint32_t ds[4][NG / 2];
 #pragma unroll
       for (int i = 0; i < 4; ++i) steps<Dv>(tile + S::kVStep, 8 * i + g, ds[i]);
-      if (__builtin_expect(!have_unit, 0)) {
-        have_unit = true;
+      if (__builtin_expect(open != 0, 0)) {
 #pragma unroll
         for (int w = 0; w < NG / 2; ++w) {
           uint32_t big = 0;
@@ -642,9 +647,10 @@ attend(const __grid_constant__ AttendArgs a, const __grid_constant__ CacheView v
           big = __vmaxs2(big, __shfl_xor_sync(kAll, big, 4));
           big = __vmaxs2(big, __shfl_xor_sync(kAll, big, 8));
           big = __vmaxs2(big, __shfl_xor_sync(kAll, big, 16));
-          shift[w] = 0;
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
+            if (!((big >> (16 * k)) & 0xffffu) || !((open >> (2 * w + k)) & 1)) continue;
+            open &= ~(1u << (2 * w + k));
             const int ex = min(max((int)((big >> (16 * k + 7)) & 255u) - 127, -40), 60);
             unit[2 * w + k] = ldexpf(1.f, -3 - ex);
             // with float16's exponent: 112 less than bfloat16's
@@ -700,7 +706,7 @@ attend(const __grid_constant__ AttendArgs a, const __grid_constant__ CacheView v
         float *to = sum + (ts * RT * 8 + row) * C::kSumRow + g;
 #pragma unroll
         for (int j = 0; j < Dv / 16; ++j) {
-          const float back = have_unit ? 1.f / unit[j >> 1] : 0.f;
+          const float back = 1.f / unit[j >> 1];
           to[16 * j] = acc.o[nb][j][e] * back;
           to[16 * j + 8] = acc.o[nb][j][2 + e] * back;
         }
