@@ -3,8 +3,9 @@
 // Pair i of a row turns by t = pos[axis(i)] * f_i.  Far positions lose their angle in
 // float32 (pos * f has 24 bits, of which the turns take all but a few), so the angle is kept
 // as a fraction of a turn in 64-bit integers: pos * turn[i] modulo 2^64 drops whole turns
-// exactly, and its high 32 bits, as a float in [-1, 1) half turns, go to sincospif (error
-// below 2^-24 half turns and the function's own).
+// exactly, and its high 32 bits are half turns in [-1, 1).  Their float goes to sincospif, and what it
+// rounded off (up to 2^-25 half turns, a thousandth of a sine next to zero) turns the result by that
+// much more, so that an angle is off by 2^-31 half turns and the function's own error.
 //
 // Memory-bound: every element is read and written once.  The angles of a row are the same for
 // every head, so a thread keeps its sines and cosines and walks the heads, four at a time, with
@@ -33,7 +34,14 @@ __device__ __forceinline__ void angle(const RopeTable &t, const int32_t *pos, in
                                       float &s, float &c) {
   const int64_t p = pos[(int64_t)t.axis[i] * N];
   const uint64_t ph = (uint64_t)p * t.turn[i];
-  sincospif((float)(int32_t)(ph >> 32) * 0x1p-31f, &s, &c);
+  const int32_t half_turns = (int32_t)(ph >> 32);
+  const float x = __int2float_rn(half_turns);
+  // 2^31 does not come back as an integer: it is off by one
+  const float rest = (float)(half_turns - __float2int_rn(x)) * (3.14159265f * 0x1p-31f);
+  float s0, c0;
+  sincospif(x * 0x1p-31f, &s0, &c0);
+  s = fmaf(c0, rest, s0);
+  c = fmaf(-s0, rest, c0);
 }
 
 // VEC elements as one load; streamed, since nothing is read twice.

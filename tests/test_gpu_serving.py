@@ -1020,3 +1020,20 @@ def test_values_that_begin_with_zeros_take_the_straight_way_after_them():
     m.muse_cache_write(s.cache, K, V.expand(B, Hkv, T, D), s.table, ints([0] * B))
     assert duration(call) < 1.25 * plain
     ok()
+
+
+@pytest.mark.parametrize("flags", [0, m.MUSE_ROPE_ADJACENT, m.MUSE_ROPE_INVERSE])
+def test_rope_keeps_the_digits_of_a_small_sine(flags):
+    """(1, 0) turned by every angle: its sine is off by a relative step or two (the function's, 2u each,
+    and the result's rounding) and by an angle of 2^-31 half turns twice (the turn's 32 bits, the
+    remainder of a rounded half turn), pi 2^-30, also where it is small; an angle rounded to float32 is
+    off by pi 2^-25 there."""
+    N, D, sec, base = 20000, 64, (1,), 1.0
+    pos = np.arange(N)[None, None]
+    X = torch.zeros(1, 1, N, D, device="cuda")
+    X[..., 0] = 1
+    y = host(m.muse_rope_axes(X, ints(pos), sec, base, flags=flags))[..., :2]
+    ref = so.rope(host(X), pos, sec, base, inverse=bool(flags & 1), adjacent=bool(flags & 2))[..., :2]
+    assert (np.abs(ref[..., 1]) < 2.0 ** -10).sum() > 5
+    assert (np.abs(y - ref) <= 6 * U * np.abs(ref) + np.pi * 2.0 ** -30 + N * 2.0 ** -53).all()
+    ok()
