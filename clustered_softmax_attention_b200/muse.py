@@ -445,9 +445,10 @@ def muse_cache_tile_bytes(D: int, Dv: int) -> int:
 
 
 def muse_cache_shape(pages: int, Hkv: int, page: int, D: int, Dv: int):
-    """Shape of the uint8 tensor that holds a cache: [pages, Hkv, page/32, tile bytes]."""
+    """Shape of the uint8 tensor that holds a cache: [pages, Hkv, page/32, tile bytes].  page is a
+    power of two, 32 to 1024."""
     n = muse_cache_tile_bytes(D, Dv)
-    if n == 0 or page % 32:
+    if n == 0 or pages < 1 or Hkv < 1 or not 32 <= page <= 1024 or page & (page - 1):
         raise MuseError(2, "muse_cache_shape")
     return pages, Hkv, page // 32, n
 

@@ -217,3 +217,14 @@ def test_the_hook_of_the_many_row_form_is_a_bit_of_its_own(lib):
     assert m.MUSE_TEST_WITHHOLD_CACHE == 4 and m.MUSE_TEST_WITHHOLD_VALUES == 1
     for bits in (2, 6, 8, 4 | 8, 1 << 31):
         assert lib.muse_set_test_hooks(bits, 0) == 1
+
+
+@pytest.mark.parametrize("pages,Hkv,page", [(10, 4, 96), (10, 4, 0), (10, 4, 16), (10, 4, 2048), (10, 4, -32),
+                                            (0, 4, 64), (10, 0, 64), (-1, 4, 64)])
+def test_no_shape_for_a_cache_that_every_call_refuses(lib, pages, Hkv, page):
+    with pytest.raises(m.MuseError, match="SHAPE"):
+        m.muse_cache_shape(pages, Hkv, page, 64, 64)
+    c = _c(pages=pages, Hkv=Hkv, page=page)
+    assert lib.muse_cache_write(_r(), _r(), _d(H=max(Hkv, 1)), c, FAKE, None, ST) == 2
+    for good in (32, 64, 1024):
+        assert m.muse_cache_shape(10, 4, good, 64, 64) == (10, 4, good // 32, 2304)
