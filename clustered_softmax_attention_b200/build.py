@@ -78,10 +78,28 @@ def build(verbose: bool = False, ptxas_info: bool = False, force: bool = False) 
     return OUT
 
 
+def _binding_made_for() -> str:
+    """What _serving.so depends on besides its sources: an extension of another interpreter or torch
+    does not load, or loads and breaks."""
+    import torch
+
+    return f"{sys.implementation.cache_tag} {sys.version} torch {torch.__version__} {torch.__file__}"
+
+
+def _binding_stale() -> bool:
+    stamp = os.path.join(BUILD_DIR, "binding.stamp")
+    if _stale(BINDING, os.path.join(CSRC, "binding.cpp"), [os.path.join(ROOT, "include", "muse.h")]):
+        return True
+    if not os.path.exists(stamp):
+        return True
+    with open(stamp) as f:
+        return f.read() != _binding_made_for()
+
+
 def _build_binding(verbose: bool, force: bool) -> None:
     """csrc/binding.cpp against this interpreter and its torch, linked to libmuse.so."""
     src = os.path.join(CSRC, "binding.cpp")
-    if not force and not _stale(BINDING, src, [os.path.join(ROOT, "include", "muse.h")]):
+    if not force and not _binding_stale():
         return
     import sysconfig
 
@@ -101,6 +119,8 @@ def _build_binding(verbose: bool, force: bool) -> None:
         sys.stderr.write(" ".join(cmd) + "\n" + r.stdout + r.stderr)
     if r.returncode:
         raise RuntimeError("the binding did not build")
+    with open(os.path.join(BUILD_DIR, "binding.stamp"), "w") as f:
+        f.write(_binding_made_for())
 
 
 if __name__ == "__main__":

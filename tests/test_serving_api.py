@@ -228,3 +228,23 @@ def test_no_shape_for_a_cache_that_every_call_refuses(lib, pages, Hkv, page):
     assert lib.muse_cache_write(_r(), _r(), _d(H=max(Hkv, 1)), c, FAKE, None, ST) == 2
     for good in (32, 64, 1024):
         assert m.muse_cache_shape(10, 4, good, 64, 64) == (10, 4, good // 32, 2304)
+
+
+def test_the_binding_is_built_again_for_another_torch_or_interpreter(tmp_path, monkeypatch):
+    from clustered_softmax_attention_b200 import build as b
+
+    stamp = tmp_path / "binding.stamp"
+    so = tmp_path / "_serving.so"
+    so.write_bytes(b"")          # newer than its sources
+    monkeypatch.setattr(b, "BUILD_DIR", str(tmp_path))
+    monkeypatch.setattr(b, "BINDING", str(so))
+    assert b._binding_stale()    # nobody knows for what it was built
+    stamp.write_text(b._binding_made_for())
+    assert not b._binding_stale()
+    for where, name, other in ((torch, "__version__", "0.0"), (b.sys, "version", "3.0")):
+        with monkeypatch.context() as c:
+            c.setattr(where, name, other)
+            assert b._binding_stale()
+    assert not b._binding_stale()
+    so.unlink()
+    assert b._binding_stale()
