@@ -433,7 +433,9 @@ def muse_rope_axes(Q, positions, sections, base: float = 10000.0, K=None, flags:
     """Rotary positions with several axes: Q [B,H,N,D] (and K [B,Hk,N,D]) turned by positions
     int32 [B,axes,N] (or [axes,N], shared by the batch); sections: the pairs of each axis.
     Returns out, or (out, k_out) with K.  out may be Q itself, k_out K itself.  With
-    MUSE_ROPE_INVERSE it turns back, which is the gradient."""
+    MUSE_ROPE_INVERSE it turns back, which is the gradient: like every call here it is outside
+    autograd (what it returns requires no grad, whatever Q does), and a training graph calls it
+    from the forward and the backward of a torch.autograd.Function."""
     r = (_SERVING or _serving()).rope_axes(Q, positions, sections, base, K, flags, out, k_out)
     if r.__class__ is int:
         _check(r, "muse_rope_axes")

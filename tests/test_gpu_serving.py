@@ -1037,3 +1037,66 @@ def test_rope_keeps_the_digits_of_a_small_sine(flags):
     assert (np.abs(ref[..., 1]) < 2.0 ** -10).sum() > 5
     assert (np.abs(y - ref) <= 6 * U * np.abs(ref) + np.pi * 2.0 ** -30 + N * 2.0 ** -53).all()
     ok()
+
+
+class Turned(torch.autograd.Function):
+    """muse_rope_axes in a training graph."""
+
+    @staticmethod
+    def forward(ctx, Q, K, pos, flags):
+        ctx.save_for_backward(pos)
+        ctx.flags = flags
+        return m.muse_rope_axes(Q, pos, (8, 12, 12), 100.0, K=K, flags=flags)
+
+    @staticmethod
+    def backward(ctx, dQ, dK):
+        return (*m.muse_rope_axes(dQ.contiguous(), ctx.saved_tensors[0], (8, 12, 12), 100.0, K=dK.contiguous(),
+                                  flags=ctx.flags ^ m.MUSE_ROPE_INVERSE), None, None)
+
+
+@pytest.mark.parametrize("flags", [0, m.MUSE_ROPE_ADJACENT | m.MUSE_ROPE_AXIS_LADDER])
+def test_rope_in_a_training_graph(flags):
+    """Logits of turned queries and keys, keys shared by query heads: gradients against the same graph
+    of float64 torch operations, in which a rotation is a product with its matrix.  A product's sums of
+    64 and of N H terms in float32 are off by (64 + 2 N) u of their terms' sizes, a rotation as in
+    rope_close (under 12 u); 256 u of the sizes that the gradients' terms reach."""
+    B, H, Hk, N, D = 2, 4, 2, 9, 64
+    Q, K = randn(1, B, H, N, D).requires_grad_(), randn(2, B, Hk, N, D).requires_grad_()
+    pos = np.random.default_rng(0).integers(-50, 50, (B, 3, N))
+    kw = dict(adjacent=bool(flags & 2), axis_ladder=bool(flags & 4))
+    q, k = Turned.apply(Q, K, ints(pos), flags)
+    assert q.requires_grad and not m.muse_rope_axes(Q, ints(pos), (8, 12, 12), flags=flags).requires_grad
+    W = randn(3, B, H, N, N)
+    ((q @ k.repeat_interleave(H // Hk, 1).transpose(-1, -2)) * W).sum().backward()
+    eye = np.broadcast_to(np.eye(D)[None, :, None], (B, D, N, D))
+    R = torch.tensor(so.rope(eye, pos, (8, 12, 12), 100.0, **kw)).permute(0, 2, 1, 3)  # [B, N, in, out]
+    Q64, K64 = (x.detach().double().cpu().requires_grad_() for x in (Q, K))
+    q64, k64 = (torch.einsum("bhnd,bnde->bhne", x, R) for x in (Q64, K64))
+    ((q64 @ k64.repeat_interleave(H // Hk, 1).transpose(-1, -2)) * W.double().cpu()).sum().backward()
+    for got, want, other in ((Q.grad, Q64.grad, K), (K.grad, K64.grad, Q)):
+        size = 2 * float(W.abs().sum(-1).max()) * float(other.detach().abs().max()) * H
+        assert (host(got) - want.numpy() <= 256 * U * size).all() and (want.numpy() - host(got) <= 256 * U * size).all()
+    ok()
+
+
+@pytest.mark.parametrize("H,M,dtype", [(16, 1, BF16), (16, 1, F32), (16, 8, BF16), (16, 40, BF16)])
+def test_stretches_on_two_streams_at_once(H, M, dtype):
+    """A table too long for clusters, and the form for many rows: partial sums and the join that reads
+    them, on two streams with a workspace each, repeat what one stream gives."""
+    s = filled(2, 2, 64, 400, 128, 128, 6000)
+    Qs = [randn(i, 2, H, M, 128, dtype=dtype) for i in range(6)]
+    lens = [ints([6000, 4500]), ints([77, 6000])]
+    call = lambda q, i, ws: m.muse_cache_attend(q, s.cache, s.table, lens[i % 2], scale=0.09, ws=ws)
+    wss = [m.workspace("muse_cache_attend", m.dims(Qs[0]), 2) for _ in range(2)]
+    ref = [[x.clone() for x in call(q, i, wss[0])] for i, q in enumerate(Qs)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = []
+    for i, q in enumerate(Qs * 4):
+        k = (i // 2 + i) % 2
+        with torch.cuda.stream(streams[k]):
+            got.append(call(q, i, wss[k]))
+    torch.cuda.synchronize()
+    for i, pair in enumerate(got):
+        assert all(torch.equal(a, b) for a, b in zip(pair, ref[i % 6])), i
+    ok()
