@@ -495,7 +495,6 @@ attend(const __grid_constant__ AttendArgs a, const __grid_constant__ CacheView v
       unit[w] = 1.f;
       shift[w >> 1] = 0;
     }
-    bool far = false;
 
     int tok = (sp.t0 + ts) * kTile - TS * kTile;
     for (int it = 0; it < n_it; ++it) {
@@ -577,7 +576,6 @@ attend(const __grid_constant__ AttendArgs a, const __grid_constant__ CacheView v
           move |= __fmul_rn(top[nb][e], rf[nb][e]) - mx[nb][e] > 14.f;
         }
       if (__builtin_expect(__any_sync(kAll, move), 0)) {
-        far = false;
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -589,7 +587,6 @@ attend(const __grid_constant__ AttendArgs a, const __grid_constant__ CacheView v
             const float now = fmaxf(mx[nb][e], __fsub_ru(__fmul_rn(y, rf[nb][e]), 9.f));
             const float fix = now == -CUDART_INF_F ? 1.f : ex2(mx[nb][e] - now);
             mx[nb][e] = now;
-            far |= fabsf(now) > kFar && now != -CUDART_INF_F;
             l[nb][e] *= fix;
 #pragma unroll
             for (int j = 0; j < Dv / 16; ++j) {
@@ -597,25 +594,14 @@ attend(const __grid_constant__ AttendArgs a, const __grid_constant__ CacheView v
               acc.o[nb][j][2 + e] *= fix;
             }
           }
-        far = __any_sync(kAll, far);
       }
-      if (__builtin_expect(far, 0)) {
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
+      for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int e = 0; e < 2; ++e)
-              tk.p[nb][i][e] = ex2(__fmul_rn(tk.p[nb][i][e], rf[nb][e]) - mx[nb][e]);
-      } else {
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-              tk.p[nb][i][e] = ex2(fmaf(tk.p[nb][i][e], rf[nb][e], -mx[nb][e]));
-      }
+          for (int e = 0; e < 2; ++e)
+            tk.p[nb][i][e] = ex2(__fmul_rn(tk.p[nb][i][e], rf[nb][e]) - mx[nb][e]);
       if (__builtin_expect(hide.edge, 0)) {
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)

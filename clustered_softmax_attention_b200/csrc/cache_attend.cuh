@@ -171,9 +171,10 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// A weight is 2^(x r - m), in one rounding; beyond 2^20 that is no longer by the rounded logits x r that
-// the reference m was taken from (half a step of 2^28 is 16), so there x r is rounded first.  m itself,
-// 9 below a logit, is rounded upwards, so that no weight passes 2^14.
+// A weight is 2^(x r - m) with x r rounded, as it was when the reference m was taken: by the unrounded
+// product a logit of 2^28 would be off by up to 16, and its weight past what float16 holds.  m, 9 below a
+// logit, is rounded upwards.  The tcgen05 form, which has 128 weights a row and tile, rounds product and
+// difference once as long as its references are below kFar, where that is off by 2^-4 at most.
 constexpr float kFar = 0x1p20f;
 // (x & mask) | with in one operation (written out, it becomes two).
 template <uint32_t kMask>
