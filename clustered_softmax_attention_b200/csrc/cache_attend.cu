@@ -438,8 +438,8 @@ attend(const __grid_constant__ AttendArgs a, const __grid_constant__ CacheView v
       // NaN is NaN.
       const int e = min(max((int)(top >> 23) - 127 - 14, -114), 113);
       const float mul = bad ? CUDART_NAN_F : a.scale < 0.f ? -ldexpf(1.f, -e) : ldexpf(1.f, -e);
-      // logits in units of log 2
-      const float rfg = fmaxf(ldexpf(fabsf(a.scale) * 1.44269504f, e), 1e-37f);
+      // logits in units of log 2; above zero, so that what is hidden stays -infinity
+      const float rfg = fmaxf(ldexpf(fabsf(a.scale) * 1.44269504f, e), 1e-45f);
       const int row0 = sp.rb * C::kRows + rt * C::kTileRows + 8 * nb;
 #pragma unroll
       for (int k = 0; k < 2; ++k) {

@@ -621,8 +621,8 @@ attend_tc(const __grid_constant__ AttendArgs a, const __grid_constant__ CacheVie
         const uint2 odd = *reinterpret_cast<const uint2 *>(sm.odd[st]);
         auto is = [&](int c, uint32_t what) { return ((c < 4 ? odd.x : odd.y) >> (8 * (c & 3))) & what; };
         const bool edge = see_all - t * kTok < kTok || ((odd.x | odd.y) & (0x01010101u * kGone));
-        // to logits in units of log 2
-        auto to2 = [&](int c) { return fmaxf(sm.scale[st][c] * rf, 1e-37f); };
+        // to logits in units of log 2; above zero, so that what is hidden stays -infinity
+        auto to2 = [&](int c) { return fmaxf(sm.scale[st][c] * rf, 1e-45f); };
         float sums[2] = {0.f, 0.f};
         // The reference moves: what was summed and weighed by it, the tile's first `done` chunks of
         // weights among them, is brought to the new one.

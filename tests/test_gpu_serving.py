@@ -1100,3 +1100,23 @@ def test_stretches_on_two_streams_at_once(H, M, dtype):
     for i, pair in enumerate(got):
         assert all(torch.equal(a, b) for a, b in zip(pair, ref[i % 6])), i
     ok()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("H,M", [(4, 1), (4, 16), (4, 40)])
+@pytest.mark.parametrize("qk", [(96, -96, 0), (98, 0, -112), (-100, 100, 0), (0, 0, -140)])
+def test_the_ends_of_the_range(qk, H, M, dtype):
+    """Keys, queries and the scale as far apart as float32 has them, values of 2^-60 and then of 2^46: as
+    attend_close (scale times 2^-14 was held above 2^-123, which keys of 2^98 show)."""
+    T, (k, q, c) = 300, qk
+    s = Store(1, 1, 32, 10, 64, 64)
+    K, V = randn(1, 1, 1, T, 64) * 2.0 ** k, randn(2, 1, 1, T, 64)
+    V[:, :, :140] *= 2.0 ** -60
+    V[:, :, 140:] *= 2.0 ** 46
+    m.muse_cache_write(s.cache, K, V, s.table, ints([0]))
+    Q = (randn(3, 1, H, M, 64) * 2.0 ** q).to(dtype)
+    scale = 0.1 * 2.0 ** c
+    for length in (T, 130):
+        out, lse = m.muse_cache_attend(Q, s.cache, s.table, ints([length]), scale=scale)
+        attend_close(host(out), host(lse), Q, s, [length], [M], scale, dtype)
+    ok()
