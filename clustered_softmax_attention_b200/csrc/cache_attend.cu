@@ -17,12 +17,12 @@
 // can be long, a cluster of CTAs takes an item instead and joins its sums through distributed
 // shared memory: one launch.
 //
-// What bounds it, bfloat16 rows of 128 + 128 channels: up to 8 rows a cache head a 32-token tile
-// costs the card 0.9 ns, 5.2 TB/s of codes (79 % of a copy's rate); it is the instructions that
-// turn codes into operands (660 a tile; ALU 43 %, tensor pipe 22 %, issue slots about half used), not DRAM
-// (48 %).  Two sequences of 65536 tokens, 16 heads: 79 us, of which 59 are tiles and 20 are not:
-// setting up, the first tile's way, 7 us of joining.  8 x 8 heads of 32768 tokens: 86 us with up to 8
-// rows, 109 with 16, 199 with 32, 358 with 64: codes are dequantised by every warp for its 16 rows.
+// What bounds it, bfloat16 rows of 128 + 128 channels: up to 8 rows a cache head a further 32-token
+// tile costs the card 1.03 ns (4.5 TB/s of codes); it is the instructions that turn codes and weights
+// into operands (746 a tile; ALU 39 %, tensor pipe 29 %, issue slots about half used), not DRAM (44 %).
+// Two sequences of 65536 tokens, 16 heads: 87 us, 3.5 TB/s, 53 % of a copy's rate, of which 68 are tiles
+// and 19 are not: setting up, the first tile's way, 6 us of joining.  A tile with 16, 32 and 64 rows:
+// 1.6, 3.3 and 6.4 ns: codes are dequantised by every warp for its 16 rows.
 #include <algorithm>
 #include <atomic>
 
@@ -34,11 +34,12 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kCluster = 8;      // CTAs of a cluster that takes an item
 // Clusters take tables of up to so many 32-token tiles a token slice (a sequence's CTAs are fixed
-// beforehand, so a ragged batch waits for its longest): 8 sequence heads of 4000 tokens 18 us in
-// stretches, 12 here; 32 of 8000: 31 and 25, ragged 25 and 23; of 16000: 41 and 35, ragged 35 and 33,
-// but two of 16 heads 27 and 27.  Float32 rows, whose tiles take three times as long: 9 of 4000
-// tokens 18 and 14, of 8000 23 and 23, of 16000 27 and 33.  More CTAs than fit at once: 56 of 8000
-// tokens 37 and 45; only short tables then (56 of 1000: 23 either way).
+// beforehand, so a ragged batch waits for its longest).  In stretches and here, us behind a flushed
+// L2: 8 heads of 4000 tokens 21 and 16; 4 x 8 of 8000 30 and 27, ragged or not; 4 x 8 of 16000 40 and 39,
+// ragged 36 and 37.  Float32 rows, whose tiles take three times as long: 9 heads of 4000 tokens 19 and 16,
+// of 8000 24 and 22, of 16000 28 and 33.  More CTAs than fit at once: 7 x 8 heads of 8000 tokens 38 and
+// 48; only short tables then (of 1000: 24 and 25).  It goes by the table, whose width the host knows: a
+// sequence of 1000 tokens in a table of 65536 takes 17 us in stretches, in one of its own size 14.
 template <typename T>
 constexpr int kClusterTiles = sizeof(T) == 4 ? 32 : 64;
 constexpr int kClusterTilesTwice = 16;

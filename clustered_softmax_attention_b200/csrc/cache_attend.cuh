@@ -50,9 +50,12 @@ __device__ __forceinline__ int seq_tiles(const AttendArgs &a, const CacheView &v
 }
 
 // Beginning and ending an item (its queries, joining its sums) takes a CTA as long as kItemTiles
-// tiles: so many places on the line come before each item's tiles.  With 8, 12, 16, 20 and 28: 48
-// sequences of up to 8192 tokens, 8 heads, 91 81 76 71 74 us; 64 of up to 4096 with 16 rows a head,
-// 102 92 88 84 85; 200 of up to 2048, 119 115 105 102 100; 2 of 65536, 16 heads, 82 80.5 80 79.5 79.
+// tiles: so many places on the line come before each item's tiles.  With 8, 12, 16, 20 and 28, us behind
+// a flushed L2 (they repeat within 2): 48 sequences of up to 8192 tokens, 8 heads, 109 99 93 91 91; 64 of up
+// to 4096 with 16 rows a head, 130 112 103 103 105; 200 of up to 2048, 136 128 120 118 122; 2 of 65536, 16
+// heads, 97 95 93 93 93; float32 rows, the first batch, 122 116 118 116 120.  With 64 rows a head, whose
+// tiles take six times as long, fewer would do: 24 of up to 4096 144 151 155 161 169, float32 of up to
+// 2048 155 162 171 179 198.  Where a stretch is shorter than this, CTAs fall between the items.
 constexpr int kItemTiles = 20;
 // Row blocks of sequence b: a padded batch has sequences with fewer rows than M.
 __device__ __forceinline__ int seq_blocks(const AttendArgs &a, int b) {
@@ -184,7 +187,8 @@ __device__ __forceinline__ uint32_t picked(uint32_t x, uint32_t with) {
   return y;
 }
 // Four pairs of codes of a word (nibbles n and n + 4) as float16: 1024 + u, or 1024 + 16 u,
-// without its offset.
+// without its offset.  Small integers under the exponent of a power of two, whose mantissa they become, is
+// a published way of unpacking 4-bit weights (Y. J. Kim et al., 2022).
 __device__ __forceinline__ void codes_f16(uint32_t x, uint32_t (&c)[4]) {
   const uint32_t y = x >> 8;
   const __half2 less = __half2half2(__ushort_as_half(0xE408));     // -1032
@@ -222,8 +226,8 @@ __device__ __forceinline__ void finish_row(const AttendArgs &a, int b, int h, in
 // parts read by four warps in turn and joined in a fixed order.  It takes as long as the loads that
 // wait for one another: the ends, then references and sums together.  Four sums a thread are asked
 // for ahead, in the 40 registers of which 12 CTAs fit an SM (eight sums take 56 registers, 9 CTAs an
-// SM, and 1536 rows two waves).  References first and sums after them, against this: 2 heads x 512
-// rows over 16384 tokens 57.5 and 55.4 us a call, 2 x 16 rows over 65536 79.9 and 79.1.
+// SM, and 1536 rows two waves).  References first and sums after them took 2 us longer with 2
+// heads x 512 rows over 16384 tokens, 1 us with 2 x 16 rows over 65536.
 template <typename T, int Dv, int kRows>
 __global__ void __launch_bounds__(128, 12) attend_join(const __grid_constant__ AttendArgs a,
                                                    const __grid_constant__ CacheView v, int *status) {
@@ -311,9 +315,10 @@ __global__ void __launch_bounds__(128, 12) attend_join(const __grid_constant__ A
 }
 
 // The form for more than 64 bfloat16 rows of a cache head (cache_attend_tc.cu), in blocks of 128.
-// Beginning and ending an item, in its tiles of 128 tokens.  With 0, 3, 6, 8, 11 and 16: 2 x 2 heads of
-// 16384 tokens, 512 rows each, - 62 57.5 57.4 59.5 59 us; 48 sequences of 128 to 8000 tokens, 4 heads
-// of 128 rows, 156 115 101 101 112 128; 24 of 0 to 8191, 8 heads, 264 180 167 173 177 194.
+// Beginning and ending an item, in its tiles of 128 tokens.  With 0, 3, 6, 8, 11 and 16, us behind a
+// flushed L2: 2 x 2 heads of 16384 tokens, 512 rows each, 92 86 81 79 83 83; 48 sequences of 128 to 8000
+// tokens, 4 heads of 128 rows, 273 251 228 228 228 233; 24 of 0 to 8191, 8 heads, 300 250 225 225 222 239;
+// but 8 heads of 1024 tokens, 512 rows each, 44 46 48 50 50 52 (stretches shorter than this).
 constexpr int kTcItemTiles = 8;
 template <int D, int Dv>
 cudaError_t launch_attend_tc(AttendArgs a, const CacheView &v, int *status, cudaStream_t st);

@@ -20,15 +20,15 @@
 // four apart a register; Q is laid out alike, and the output's columns are put back at the end.
 //
 // Two sequences, two cache heads of four query heads, 128 new rows (512 rows a cache head), 128 + 128
-// channels: 55 us over 16384 tokens, of which about 23 are a call's beginning and end; from there
-// 16 ns a tile of 128 x 128 (2.4 us an SM), 524 TFLOP/s of 1640: both products are 0.8 of those 2.4 us,
-// and the way of a tile through the three roles is the rest (ALU 23 %, exponentials 17 %, no unit is
-// busy).  Eight softmax warps instead of four, and an issuer among the producers, gained nothing.
-// The other form against this one, us, 64 rows a cache head and fewer, then more:
-//   8 x 8 heads, 1024 tokens:    36 rows 37 and 45, 64 rows 39 and 49; 68 rows 56 and 49, 512 rows 161 and 119
-//   2 x 2 heads, 16384 tokens:   36 rows 37 and 39, 64 rows 39 and 39; 68 rows 46 and 37, 512 rows 110 and 70
-//   8 x 8 heads, 16384 tokens:   36 rows 195 and 166, 64 rows 199 and 168; 68 rows 390 and 170, 512 rows 1390 and 602
-//   2 x 2 heads, 1024 tokens:    36 rows 21 and 27, 64 rows 21 and 29; 68 rows 24 and 27, 512 rows 32 and 33
+// channels: 64 to 68 us over 16384 tokens, of which about 25 are a call's beginning and end; from there
+// 19 ns a tile of 128 x 128 (2.9 us an SM), 434 TFLOP/s of 1640: the three products (two of weights) are
+// 1.1 of those 2.9 us, and the way of a tile through the three roles is the rest (ALU 25 %, tensor pipe
+// 18 %, no unit is busy; stalls: loads, and instructions that are not there yet).
+// The other form against this one, us behind a flushed L2, 64 rows a cache head and fewer, then more:
+//   8 x 8 heads, 1024 tokens:    36 rows 44 and 56, 64 rows 48 and 58; 68 rows 67 and 58, 512 rows 185 and 128
+//   2 x 2 heads, 16384 tokens:   36 rows 38 and 46, 64 rows 40 and 46; 68 rows 52 and 46, 512 rows 134 and 79
+//   8 x 8 heads, 16384 tokens:   36 rows 243 and 204, 64 rows 247 and 206; 68 rows 463 and 208, 512 rows 1755 and 707
+//   2 x 2 heads, 1024 tokens:    36 rows 21 and 30, 64 rows 21 and 30; 68 rows 22 and 30, 512 rows 32 and 40
 #include <atomic>
 
 #include "cache_attend.cuh"
@@ -49,7 +49,7 @@ constexpr int kKeys = 4;    // key steps that K' does not hold
 // TMEM columns: S (two of 128), O.  A weight takes the place of its S as two float16 pieces, 21 bits:
 // sixteen tokens' columns hold eight of upper and eight of lower pieces.  In one piece (11 bits) results
 // differed from float32 arithmetic's by 9e-4 in norm, in two by 1.6e-4.  One piece and two, 128 + 128
-// channels: 2 x 2 heads of 16384 tokens, 512 rows a head, 55 and 63 us; 8 x 8 heads, 68 rows, 170 and 204
+// channels: 2 x 2 heads of 16384 tokens, 512 rows a head, 55 and 64 us; 8 x 8 heads, 68 rows, 170 and 204
 // (the second products take about 12 of the 34, the pieces and their stores the rest).
 constexpr uint32_t kS = 0, kO = 256;
 
@@ -119,7 +119,7 @@ __host__ __device__ constexpr int column_of(int c) {
 
 // The columns of S of sixteen tokens whose key steps K' does not hold, in float32 from the codes: a row a
 // thread, `q` its block of queries.  `p`: their tile of 32 tokens, whose half `part` they are; `scale`: what
-// the columns are multiplied by.  Small rather than fast (5 us), as exact_values.
+// the columns are multiplied by.  Small rather than fast (16 us), as exact_values.
 template <int D>
 __device__ __noinline__ void exact_logits(uint32_t columns, __half (*q)[kTcRows * 64], const uint8_t *p,
                                           const uint16_t *steps, int part, float scale, float *tokens) {
@@ -167,7 +167,7 @@ __device__ __noinline__ void exact_logits(uint32_t columns, __half (*q)[kTcRows 
 
 // O += p v of sixteen tokens whose value steps V' does not hold, in float32 from the codes: a row a
 // thread.  `logits`: their columns of S; `left`: tokens of them that the row sees; `p`: their tile of 32
-// tokens, whose half `part` they are; begin: O holds nothing yet.  Small rather than fast (3 us): a cold
+// tokens, whose half `part` they are; begin: O holds nothing yet.  Small rather than fast (7 us): a cold
 // kernel waits for its instructions.
 template <int D, int Dv>
 __device__ __noinline__ void exact_values(uint32_t logits, float to2, float ref, int left, const uint8_t *p,

@@ -412,7 +412,14 @@ muse_status muse_cache_read(muse_dims d, muse_cache c, const int32_t *start, con
  *   Query head h of d.H reads cache head h / (d.H / c.Hkv).  A row that sees nothing (a sequence
  *   shorter than its new rows) gives O = 0 and lse = -inf; rows from counts[b] on stay as they are.
  * Q [B,H,N,D], O [B,H,N,Dv], 1 <= N <= 128, d.H a multiple of c.Hkv; lse float32 [B,H,N] dense,
- * or NULL.  The codes enter the products as they are (integers), the steps in float32.
+ * or NULL.  What is rounded on the way, statistics and sums being float32 throughout:
+ *   bfloat16 rows, up to 64 a cache head (d.H / c.Hkv * N): codes enter the products as integers; a
+ *   key's step multiplies a float32 sum, a value's step the weight.  More rows: code * step is the
+ *   operand, exact in float16 at a power of two, and sixteen tokens for which it is not are formed in
+ *   float32.  The weights, and their products with steps, are held in two float16 pieces: 21 bits, or,
+ *   where that is coarser, 2^-29 of the group's largest value at the row's largest weight.
+ *   float32 rows: queries to 22 bits, codes as integers, weights times steps to 24 bits.
+ * Keys up to 2^100 and values up to 2^50 in magnitude; beyond, a float32 sum may overflow.
  * A length below 0 or past the table, or a page outside the cache, sets MUSE_ERR_DEVICE; those
  * tokens are left out.  Workspace: muse_workspace_size("muse_cache_attend", d, c.Hkv, ...); the
  * library leaves nothing in it that the next call needs; calls that may run at the same time need
